@@ -1,0 +1,97 @@
+// moe.h -- what the host checks (moe_host.cpp) hand to the kernels of the
+// operators around the exchange (moe_gemm.hip, moe_route.hip, moe_rows.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace a2av {
+
+// Element kinds of the grouped products.
+enum GmmType { kGmmBF16 = 0, kGmmFP16 = 1, kGmmMX4 = 2 };
+// Which operands the reduction runs along: forward (both rows), input
+// gradient (the weight's columns), weight gradient (both columns).
+enum GmmMode { kGmmFwd = 0, kGmmDx = 1, kGmmDw = 2 };
+
+struct GmmParams {
+  const uint8_t* rows;     // x or dy: the operand whose rows are the grouped rows
+  const uint8_t* other;    // w (fwd, dx) or x (dw)
+  const uint8_t* row_scales;    // MX4: [x_rows, B] and [E, N, B]
+  const uint8_t* other_scales;
+  uint8_t* out;
+  const int32_t* counts;
+  const int32_t* index;    // may be null
+  int32_t* status;         // may be null
+  int64_t row_stride;      // bytes
+  int64_t other_stride;    // bytes from one row of `other` to the next
+  int64_t out_stride;      // elements
+  int64_t x_rows;          // rows that index may name
+  int64_t nrows;           // grouped rows
+  int32_t E;
+  int32_t N, K;            // of the weights
+  int32_t blocks;          // MX4: scale blocks of a row
+  int32_t out_type;        // a2av_dtype of out
+};
+
+struct RouteParams {
+  const void* logits;
+  int64_t stride;
+  int32_t tokens, E, k, renorm, dtype;
+  int32_t* experts;
+  float* weights;
+  int32_t* counts;
+  int32_t* order;
+  int32_t* place;
+  int32_t* hist;           // workspace [blocks][E]
+};
+
+struct RouteBackParams {
+  const void* logits;
+  int64_t stride;
+  int32_t tokens, E, k, renorm, dtype;
+  const int32_t* experts;
+  const float* weights;
+  const float* dweights;
+  void* dlogits;
+};
+
+struct CombineParams {
+  const void* y;
+  const void* dout;
+  const int32_t* place;
+  const float* weights;    // may be null: every weight 1
+  void* out;               // forward
+  void* dy;                // backward
+  float* dweights;         // backward; may be null
+  int32_t* status;
+  int64_t y_stride, o_stride, dy_stride;  // elements; o_stride of out or dout
+  int64_t y_rows;
+  int32_t tokens, k, width, dtype;
+};
+
+struct Mx4Params {
+  const void* x;
+  void* out;
+  const uint8_t* codes_in;
+  const uint8_t* scales_in;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t stride;
+  int32_t rows, cols, blocks, dtype;
+};
+
+hipError_t launch_gmm(const GmmParams& p, GmmType type, GmmMode mode, hipStream_t stream);
+hipError_t launch_route(const RouteParams& p, hipStream_t stream);
+hipError_t launch_route_back(const RouteBackParams& p, hipStream_t stream);
+hipError_t launch_combine(const CombineParams& p, hipStream_t stream);
+hipError_t launch_combine_back(const CombineParams& p, hipStream_t stream);
+hipError_t launch_mx4_quantize(const Mx4Params& p, hipStream_t stream);
+hipError_t launch_mx4_dequantize(const Mx4Params& p, hipStream_t stream);
+
+// Tokens that one workgroup of the router's first kernel takes.
+constexpr int kRouteTokens = 64;
+// Up to this many slots the router is one workgroup and needs no workspace.
+constexpr int kRouteSmall = 1024;
+
+}  // namespace a2av
