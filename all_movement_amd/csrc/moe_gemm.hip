@@ -30,6 +30,7 @@ typedef float float4v __attribute__((ext_vector_type(4)));
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int8v __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
 
 // What a load reads in place of bytes past an operand's end.
 __device__ const uint32_t g_zeros[4] = {0, 0, 0, 0};
@@ -50,15 +51,22 @@ __device__ inline void wait_loads_and_barrier() {
   asm volatile("" ::: "memory");
 }
 
-__device__ inline int wave_scan(int v) {  // inclusive, 64 lanes
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    if (lane >= d) v += u;
-  }
+// Inclusive sum over the wave, by lane moves inside rows of 16 and from row to
+// row.
+__device__ inline int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31
   return v;
 }
+
+__device__ inline int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// Row tiles of c rows; c may be 2^31 - 1.
+__device__ inline int tiles_of(int c, int BM) { return c > 0 ? (c - 1) / BM + 1 : 0; }
 
 // Where a tile of grouped rows lies: expert e, rows [row0, row0 + m).
 struct Span {
@@ -67,66 +75,175 @@ struct Span {
   int64_t row0;
 };
 
-// Row tiles of c rows; c may be 2^31 - 1.
-__device__ inline int tiles_of(int c, int BM) { return c > 0 ? (c - 1) / BM + 1 : 0; }
+// The counts of 64 experts from `b` on, one per lane, with the sums before
+// them; every wave does this for itself.
+struct Counts {
+  int c;          // this lane's count
+  int rows, tiles;  // inclusive sums over the 64
+  int64_t rows_before = 0, tiles_before = 0;
 
-// Checks the counts; false when one is negative or they sum to more than
-// nrows.  total_tiles: row tiles of BM over all experts.  Every wave does it
-// for itself, 64 counts at a time.
-__device__ inline bool check_counts(const int32_t* counts, int E, int64_t nrows, int BM,
-                                    int64_t* total_tiles) {
-  const int lane = threadIdx.x & 63;
-  int64_t rows = 0, tiles = 0;
-  bool ok = true;
-  for (int b = 0; b < E; b += 64) {
-    const int c = b + lane < E ? counts[b + lane] : 0;
-    ok = ok && __ballot(c < 0) == 0;
-    // Two halves of 16 bits each keep the wave's sums inside 32 bits.
-    const int lo = __shfl(wave_scan(c & 0xffff), 63), hi = __shfl(wave_scan(c >> 16), 63);
-    rows += int64_t(lo) + (int64_t(hi) << 16);
-    ok = ok && rows <= nrows;
-    if (!ok) return false;
-    tiles += __shfl(wave_scan(tiles_of(c, BM)), 63);
+  // Takes the next 64; false when one is negative or the sum passes nrows.
+  __device__ bool take(const int32_t* counts, int E, int b, int BM, int64_t nrows) {
+    const int lane = threadIdx.x & 63;
+    c = b + lane < E ? counts[b + lane] : 0;
+    if (__ballot(c < 0)) return false;
+    // Two halves of 16 bits each keep the sums inside 32 bits.
+    const int lo = wave_scan(c & 0xffff), hi = wave_scan(c >> 16);
+    const int64_t sum = int64_t(lane_value(lo, 63)) + (int64_t(lane_value(hi, 63)) << 16);
+    if (rows_before + sum > nrows) return false;
+    rows = lo + (hi << 16);
+    tiles = wave_scan(tiles_of(c, BM));
+    return true;
   }
-  *total_tiles = tiles;
+  __device__ void pass() {
+    rows_before += lane_value(rows, 63);
+    tiles_before += lane_value(tiles, 63);
+  }
+  __device__ Span at(int b, int lane) const {
+    const int cl = lane_value(c, lane);
+    return Span{b + lane, cl, rows_before + lane_value(rows, lane) - cl};
+  }
+};
+
+// The block of the output that a workgroup computes: rows out_row0 .. + rm of
+// the output (dw: of the expert's matrix), columns c0 .. + cn.
+struct Tile {
+  Span span;
+  int64_t out_row0, c0;
+  int rm, cn;
+};
+
+// Checks the counts and finds this workgroup's tile; false when it has none.
+// Tiles stand in groups of kGroup row tiles that walk the columns together, and
+// 32 in a row go to one XCD (workgroups go round the 8 XCDs in turn, each with
+// 32 CUs and an L2 of its own), the next 32 to the next: an expert with many
+// rows is spread over all of them.
+// SPLIT, for tiles that fill a CU: what is left after whole rounds of 256 tiles,
+// when it is at most half a round, is cut into quarters, so that the last round
+// is not a whole tile long for a few CUs while the others have none (16384 rows
+// of 16 experts, 2048 x 7168, bf16: 2.25 rounds; 550 us in whole tiles).
+// *part is the quarter, -1 for a whole tile.
+template <int MODE, int BM, int BN, bool SPLIT>
+__device__ inline bool find_work(const GmmParams& p, Tile* t, int* part) {
+  Counts k;
+  bool ok = true;
+  for (int b = 0; b < p.E && ok; b += 64) {
+    if (b) k.pass();
+    ok = k.take(p.counts, p.E, b, BM, p.nrows);
+  }
+  if (!ok) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.status)
+      *p.status = A2AV_ERR_INVALID_ARGS;
+    return false;
+  }
+  const int64_t row_tiles = k.tiles_before + lane_value(k.tiles, 63);
+  const int64_t out_cols = MODE == kGmmFwd ? p.N : p.K;
+  const int64_t col_tiles = (out_cols + BN - 1) / BN;
+  const int64_t per_e = (p.N + BM - 1) / BM;  // dw: row tiles of an expert
+  const int64_t tm_all = MODE == kGmmDw ? int64_t(p.E) * per_e : row_tiles;
+  const int64_t total = tm_all * col_tiles;
+  const int64_t wg = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+  const int64_t whole = total / 256 * 256, rest = total - whole;
+  const bool cut = SPLIT && rest <= 128;
+  int64_t tile;
+  *part = -1;
+  if (wg < whole) {
+    tile = ((wg >> 8) * 8 + (wg & 7)) * 32 + (wg >> 3 & 31);
+  } else {
+    const int64_t n = cut ? rest * 4 : rest, per = (n + 7) / 8;
+    const int64_t i = (wg - whole) >> 3, u = ((wg - whole) & 7) * per + i;
+    if (i >= per || u >= n) return false;
+    tile = whole + (cut ? u >> 2 : u);
+    if (cut) *part = int(u & 3);
+  }
+  constexpr int kGroup = 4;
+  const int64_t grp = tile / (kGroup * col_tiles);
+  const int64_t in_grp = tile - grp * kGroup * col_tiles;
+  const int64_t grp_rows = tm_all - grp * kGroup < kGroup ? tm_all - grp * kGroup : kGroup;
+  const int64_t tm = grp * kGroup + in_grp % grp_rows;
+  const int64_t tn = in_grp / grp_rows;
+  const int want = MODE == kGmmDw ? int(tm / per_e) : 0;
+  int b = 0;
+  if (p.E > 64) {  // the counts again, as far as the tile's expert
+    k = Counts{};
+    k.take(p.counts, p.E, 0, BM, p.nrows);
+    while (MODE == kGmmDw ? b + 64 <= want : k.tiles_before + lane_value(k.tiles, 63) <= tm) {
+      k.pass();
+      b += 64;
+      k.take(p.counts, p.E, b, BM, p.nrows);
+    }
+  }
+  if constexpr (MODE == kGmmDw) {
+    t->span = k.at(b, want - b);
+    t->out_row0 = (tm - want * per_e) * BM;
+    t->rm = int(p.N - t->out_row0 < BM ? p.N - t->out_row0 : BM);
+  } else {
+    const uint64_t past = __ballot(k.tiles_before + k.tiles > tm);
+    const int lane = __ffsll((unsigned long long)past) - 1;
+    t->span = k.at(b, lane);
+    const int first = lane ? lane_value(k.tiles, lane - 1) : 0;
+    const int off = int(tm - k.tiles_before - first) * BM;
+    t->span.row0 += off;
+    t->span.m -= off;
+    if (t->span.m > BM) t->span.m = BM;
+    t->out_row0 = t->span.row0;
+    t->rm = t->span.m;
+  }
+  t->c0 = tn * BN;
+  t->cn = int(out_cols - t->c0 < BN ? out_cols - t->c0 : BN);
+  if (*part >= 0) {
+    const int r = (*part & 1) * (BM / 2), c = (*part >> 1) * (BN / 2);
+    if (r >= t->rm || c >= t->cn) return false;
+    t->out_row0 += r;
+    if (MODE != kGmmDw) t->span.row0 += r;
+    t->rm = t->rm - r < BM / 2 ? t->rm - r : BM / 2;
+    t->c0 += c;
+    t->cn = t->cn - c < BN / 2 ? t->cn - c : BN / 2;
+  }
   return true;
 }
 
-// The row tile `t` (counts checked).
-__device__ inline Span find_tile(const int32_t* counts, int E, int BM, int64_t t) {
-  const int lane = threadIdx.x & 63;
-  int64_t rows = 0, tiles = 0;
-  for (int b = 0; b < E; b += 64) {
-    const int c = b + lane < E ? counts[b + lane] : 0;
-    const int n = tiles_of(c, BM);
-    const int in = wave_scan(n), cs = wave_scan(c);
-    const uint64_t past = __ballot(tiles + in > t);
-    if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      const int first = __shfl(in - n, l), r0 = __shfl(cs - c, l), cl = __shfl(c, l);
-      const int off = int(t - tiles - first) * BM;
-      Span s;
-      s.e = b + l;
-      s.row0 = rows + r0 + off;
-      s.m = cl - off < BM ? cl - off : BM;
-      return s;
-    }
-    tiles += __shfl(in, 63);
-    rows += __shfl(cs, 63);
-  }
-  return Span{0, 0, 0};
+__device__ inline uint16_t round16(float v, int type) {
+  if (type == A2AV_BF16) return __builtin_bit_cast(uint16_t, __bf16(v));
+  return __builtin_bit_cast(uint16_t, _Float16(v));
 }
 
-// The rows of expert e (counts checked).
-__device__ inline Span find_expert(const int32_t* counts, int E, int e) {
-  const int lane = threadIdx.x & 63;
-  int64_t rows = 0;
-  for (int b = 0; b < e; b += 64) {
-    const int c = b + lane < e ? counts[b + lane] : 0;
-    rows += __shfl(wave_scan(c), 63);
+// A lane holds 4 columns (4g .. 4g + 3 of a fragment) of output row l16.
+template <int MODE, int TM, int TN, int FM, int FN>
+__device__ inline void store_tile(const GmmParams& p, const Tile& t, const float4v (&acc)[FM][FN],
+                                  int wm, int wn) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int64_t first = MODE == kGmmDw ? int64_t(t.span.e) * p.N + t.out_row0 : t.out_row0;
+  const bool wide = (p.out_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+#pragma unroll
+  for (int a = 0; a < FM; ++a) {
+    const int r = wm * TM + a * 16 + l16;
+    if (r >= t.rm) continue;
+#pragma unroll
+    for (int d = 0; d < FN; ++d) {
+      const int col = wn * TN + d * 16 + g * 4;
+      if (col >= t.cn) continue;
+      const int64_t at = (first + r) * p.out_stride + t.c0 + col;
+      const float4v v = acc[a][d];
+      const bool whole = wide && col + 4 <= t.cn;
+      if (p.out_type == A2AV_FP32) {
+        float* o = reinterpret_cast<float*>(p.out) + at;
+        if (whole)
+          *reinterpret_cast<float4v*>(o) = v;
+        else
+          for (int i = 0; i < 4 && col + i < t.cn; ++i) o[i] = v[i];
+      } else {
+        uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
+        uint16_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = round16(v[i], p.out_type);
+        if (whole)
+          *reinterpret_cast<uint64_t*>(o) = __builtin_bit_cast(uint64_t, h);
+        else
+          for (int i = 0; i < 4 && col + i < t.cn; ++i) o[i] = h[i];
+      }
+    }
   }
-  (void)E;
-  return Span{e, counts[e], rows};
 }
 
 // 8 elements of 16 bits at any 2-byte address, the first n of them (0..8).
@@ -147,6 +264,61 @@ __device__ inline int4v load_part(const uint8_t* p, int n) {
   return r;
 }
 
+// The same through LDS (free by now, a part of it per wave): the fragments'
+// pieces of 8 or 16 bytes become rows, which leave in whole lines.  Straight
+// from the fragments every line of the output was written in four parts, and a
+// 256 x 256 tile took 14 us to store.
+template <int MODE, int TM, int TN, int FM, int FN, int ES>
+__device__ inline void store_rows(const GmmParams& p, const Tile& t, const float4v (&acc)[FM][FN],
+                                  int wm, int wn, uint8_t* lds, int bytes) {
+  constexpr int kRow = TN * ES, kChunks = kRow / 16;
+  constexpr int kSwizzle = (kChunks < 16 ? kChunks : 16) - 1;
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int batch = bytes / (kRow * 16) < FM ? bytes / (kRow * 16) : FM;  // fragment rows at once
+  const int64_t first = MODE == kGmmDw ? int64_t(t.span.e) * p.N + t.out_row0 : t.out_row0;
+  const int64_t col0 = t.c0 + wn * TN;
+  const int cols = t.cn - wn * TN;
+  const bool wide = ((p.out_stride * ES) & 15) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+#pragma unroll
+  for (int a = 0; a < FM; ++a) {
+    const int at = a % batch;
+    uint8_t* row = lds + (at * 16 + l16) * kRow;
+#pragma unroll
+    for (int d = 0; d < FN; ++d) {
+      if constexpr (ES == 4) {
+        *reinterpret_cast<float4v*>(row + ((d * 4 + g) ^ (l16 & kSwizzle)) * 16) = acc[a][d];
+      } else {
+        uint16_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = round16(acc[a][d][i], p.out_type);
+        *reinterpret_cast<uint64_t*>(row + ((d * 2 + (g >> 1)) ^ (l16 & kSwizzle)) * 16 +
+                                     (g & 1) * 8) = __builtin_bit_cast(uint64_t, h);
+      }
+    }
+    if (at + 1 < batch && a + 1 < FM) continue;
+    constexpr int kAtOnce = 64 / kChunks;  // rows per store of the wave
+    for (int r = lane / kChunks; r < (at + 1) * 16; r += kAtOnce) {
+      const int out_row = wm * TM + (a - at) * 16 + r;
+      const int ch = lane % kChunks, col = ch * (16 / ES);
+      const int4v v = *reinterpret_cast<const int4v*>(lds + r * kRow + (ch ^ (r & kSwizzle)) * 16);
+      if (out_row >= t.rm || col >= cols) continue;
+      uint8_t* o = p.out + ((first + out_row) * p.out_stride + col0 + col) * ES;
+      if (wide && col + 16 / ES <= cols) {
+        *reinterpret_cast<int4v*>(o) = v;
+      } else if constexpr (ES == 4) {
+        for (int i = 0; i < 4 && col + i < cols; ++i) reinterpret_cast<int*>(o)[i] = v[i];
+      } else {
+        for (int i = 0; i < 8 && col + i < cols; ++i)
+          reinterpret_cast<uint16_t*>(o)[i] = uint16_t(uint32_t(v[i / 2]) >> (16 * (i & 1)));
+      }
+    }
+  }
+}
+
+// Chunk c of row r of an across tile lies at c ^ across_swizzle(r), so that the
+// transposing read, 4 rows x 32 bytes by 16 lanes, meets every bank once.
+__device__ inline int across_swizzle(int r) { return 2 * (r & 3) | (8 & r); }
+
 // One operand's tile of SPAN outputs x 128 bytes of reduction, loaded by NW
 // waves as 16-byte chunks.
 //   along:  LDS [SPAN][8 chunks], chunk c of row r at c ^ (r & 7)
@@ -163,7 +335,6 @@ struct Loader {
   int4v staged[DIRECT ? 1 : kPer];
   int wave, lane;
 
-  __device__ static int across_swizzle(int r) { return 2 * (r & 3) | (8 & r); }
   __device__ int chunk(int i) const { return (wave * kPer + i) * 64 + lane; }
   // Where chunk i lies: row of the LDS tile and chunk in that row.
   __device__ int lds_row(int i) const { return ALONG ? chunk(i) / 8 : chunk(i) / (SPAN / 8); }
@@ -191,11 +362,6 @@ __device__ inline float4v mma_mx4(int4v a, int4v b, float4v c, int sa, int sb, i
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 1, sa, 1, sb);
 }
 
-__device__ inline uint16_t round16(float v, int type) {
-  if (type == A2AV_BF16) return __builtin_bit_cast(uint16_t, __bf16(v));
-  return __builtin_bit_cast(uint16_t, _Float16(v));
-}
-
 // BM rows x BN columns of the output by WM x WN waves.
 template <int TY, int MODE, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
@@ -213,50 +379,13 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
   const int wm = wave / WN, wn = wave % WN;
   const int g = lane >> 4, l16 = lane & 15;
 
-  int64_t row_tiles = 0;
-  if (!check_counts(p.counts, p.E, p.nrows, BM, &row_tiles)) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
-    return;
-  }
-
-  // The tile of this workgroup.  Workgroups go round the 8 XCDs in turn, each
-  // with an L2 of its own: every XCD takes one contiguous eighth of the tiles.
-  const int64_t out_cols = MODE == kGmmFwd ? p.N : p.K;
-  const int64_t col_tiles = (out_cols + BN - 1) / BN;
-  const int64_t tm_all = MODE == kGmmDw ? int64_t(p.E) * ((p.N + BM - 1) / BM) : row_tiles;
-  const int64_t total = tm_all * col_tiles;
-  const int64_t per = (total + 7) / 8;
-  const int64_t wg = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
-  const int64_t in_xcd = wg / 8;
-  const int64_t tile = (wg % 8) * per + in_xcd;
-  if (in_xcd >= per || tile >= total) return;
-  constexpr int kGroup = 4;  // row tiles that walk the columns together
-  const int64_t grp = tile / (kGroup * col_tiles);
-  const int64_t in_grp = tile - grp * kGroup * col_tiles;
-  const int64_t grp_rows = tm_all - grp * kGroup < kGroup ? tm_all - grp * kGroup : kGroup;
-  const int64_t tm = grp * kGroup + in_grp % grp_rows;
-  const int64_t tn = in_grp / grp_rows;
-
-  // The output block [r0, r0 + rm) x [c0, ..) and the reduction's length.
-  Span s;
-  int64_t out_row0;
-  int rm;
-  int64_t red;
-  if constexpr (MODE == kGmmDw) {
-    const int64_t per_e = (p.N + BM - 1) / BM;
-    const int e = int(tm / per_e);
-    s = find_expert(p.counts, p.E, e);
-    out_row0 = (tm - e * per_e) * BM;
-    rm = int(p.N - out_row0 < BM ? p.N - out_row0 : BM);
-    red = s.m;
-  } else {
-    s = find_tile(p.counts, p.E, BM, tm);
-    out_row0 = s.row0;
-    rm = s.m;
-    red = MODE == kGmmFwd ? p.K : p.N;
-  }
-  const int64_t c0 = tn * BN;
-  const int cn = int(out_cols - c0 < BN ? out_cols - c0 : BN);
+  Tile t;
+  int part;
+  if (!find_work<MODE, BM, BN, false>(p, &t, &part)) return;
+  const Span s = t.span;
+  const int64_t out_row0 = t.out_row0, c0 = t.c0;
+  const int rm = t.rm, cn = t.cn;
+  const int64_t red = MODE == kGmmDw ? s.m : MODE == kGmmFwd ? p.K : p.N;
   const int steps = int((red + kStep - 1) / kStep);
 
   // ---- the loaders: where each chunk of a lane begins, without the step.
@@ -321,7 +450,37 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       ld.staged[i] = n > 0 ? load_part(ptr, n) : int4v{0, 0, 0, 0};
     }
   };
+  // dw: the rows of x of the next step to issue, read a step ahead so that
+  // their latency passes under a step's products; -1 reads zeros.
+  int next_row[MODE == kGmmDw ? c.kPer : 1];
+  auto read_rows = [&](int k) {
+    if constexpr (MODE == kGmmDw) {
+#pragma unroll
+      for (int i = 0; i < c.kPer; ++i) {
+        const int r = k * 64 + c.lds_row(i);
+        int row = -1;
+        if (r < red) {
+          row = int(s.row0 + r);
+          if (p.index) row = p.index[row];
+        }
+        next_row[i] = row;
+      }
+    }
+  };
+  auto check_rows = [&](int k) {
+    if constexpr (MODE == kGmmDw) {
+#pragma unroll
+      for (int i = 0; i < c.kPer; ++i) {
+        const int row = next_row[i];
+        if (row < 0 || row >= p.x_rows) {
+          bad_row = bad_row || k * 64 + c.lds_row(i) < red;
+          next_row[i] = -1;
+        }
+      }
+    }
+  };
   auto issue = [&](int k) {
+    check_rows(k);
     const uint32_t base = lds0 + (k & 1) * kBuf;
     constexpr auto row_kind = std::integral_constant<bool, kRowsAlong>{};
     constexpr auto col_kind = std::integral_constant<bool, kColsAlong>{};
@@ -339,16 +498,8 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       } else if constexpr (MODE == kGmmDx) {
         ptr += int64_t(k) * 64 * p.other_stride;
       } else {
-        const int64_t r = int64_t(k) * 64 + c.lds_row(i);
-        int64_t row = s.row0 + r;
-        if (p.index && r < red) {
-          row = p.index[row];
-          if (row < 0 || row >= p.x_rows) {
-            bad_row = true;
-            row = -1;
-          }
-        }
-        ptr = row < 0 ? nullptr : ptr + row * p.other_stride;
+        const int row = next_row[i];
+        ptr = row < 0 ? nullptr : ptr + int64_t(row) * p.other_stride;
       }
       load_one(c, col_kind, i, k, base + BM * 128, ptr);
     }
@@ -456,80 +607,528 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
   };
 
   if (steps > 0) {
+    read_rows(0);
     issue(0);
+    read_rows(1);
     put_staged(0);
   }
   for (int k = 0; k < steps; ++k) {
     wait_loads_and_barrier();
-    if (k + 1 < steps) issue(k + 1);
+    if (k + 1 < steps) {
+      issue(k + 1);
+      read_rows(k + 2);
+    }
     compute(k);
     if (k + 1 < steps) put_staged(k + 1);
   }
   if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
 
-  // A lane holds 4 columns (4g .. 4g + 3 of a fragment) of output row l16.
-  const int64_t out_first = MODE == kGmmDw ? e_rows + out_row0 : out_row0;
-  const bool wide = (p.out_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  store_tile<MODE, TM, TN, FM, FN>(p, t, acc, wm, wn);
+}
+
+// ------------------------------------------------------------------ the pipelined tile kernel
+
+template <int N>
+__device__ inline void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// load_to_lds with a uniform base and a 32-bit offset per lane.
+__device__ inline void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(to), "v"(offset), "s"(base)
+               : "memory");
+}
+
+// 4 bytes per lane from `src` to LDS at base + 4 * lane.
+__device__ inline void load_word_to_lds(const void* src, uint32_t base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(base), "v"(src)
+               : "memory");
+}
+
+template <class T>
+__device__ inline const T* uniform(const T* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(uint32_t(v >> 32));
+  return reinterpret_cast<const T*>(uint64_t(hi) << 32 | lo);
+}
+
+// One operand's 128 bytes x SPAN outputs of a stage in LDS, brought by wave
+// loads of 64 chunks of 16 bytes.
+//   along:  [SPAN][8 chunks], chunk c of row r at c ^ (r & 7): the 8 lanes that
+//           read 128 bytes together, one chunk of 8 rows, meet every bank once.
+//   across: 64 rows of SPAN / 8 chunks in units of one wave load (2 rows of 256
+//           outputs or 4 of 128) whose rows alternate every 32 bytes: the
+//           transposing read takes 32 bytes of 4 rows by 16 lanes, which are
+//           128 bytes in a row for SPAN 128, and for 256 two runs of 64 that
+//           the units' pitch of 1024 + 64 bytes puts into other banks.
+template <bool ALONG, int SPAN>
+struct Layout {
+  static constexpr int kRows = ALONG ? 8 : 512 / SPAN;  // LDS rows of a wave load
+  static constexpr int kPitch = !ALONG && SPAN == 256 ? 1024 + 64 : 1024;
+  static constexpr int kLoads = SPAN / 8;
+  static constexpr int kBytes = kLoads * kPitch;
+  static_assert(ALONG || SPAN == 256 || SPAN == 128, "rows of a unit");
+  // Row (of the wave load) and chunk that lane l brings.
+  __device__ static int row(int l) { return ALONG ? l >> 3 : l >> 1 & (kRows - 1); }
+  __device__ static int chunk(int l) {
+    if (ALONG) return (l ^ l >> 3) & 7;
+    return l / (2 * kRows) * 2 + (l & 1);
+  }
+  // Where a lane reads its part of the fragment of outputs 0 .. 15 in half kk
+  // of the stage; those of fragment f lie f * kFragment further.
+  static constexpr int kFragment = ALONG ? 2048 : kRows * 32;
+  // PAIRS: a lane takes chunks 2g and 2g + 1 in the two halves (any share of
+  // the chunks is right that both operands follow), so that the two scale
+  // bytes that go with them lie side by side.
+  template <bool PAIRS>
+  __device__ static uint32_t read_at(int lane, int kk) {
+    const int g = lane >> 4, l = lane & 15;
+    if (ALONG) return uint32_t(l * 128 + ((PAIRS ? 2 * g + kk : kk * 4 + g) ^ (l & 7)) * 16);
+    const int r = kk * 32 + g * 8 + (l >> 2);
+    return uint32_t(r / kRows * kPitch + (r % kRows) * 32 + (l & 3) * 8);
+  }
+  __device__ static int4v read(uint32_t at) {
+    if constexpr (ALONG) {
+      return *(const __attribute__((address_space(3))) int4v*)(uintptr_t(at));
+    } else {
+      typedef __attribute__((address_space(3))) short4v lds_short4;
+      const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(uintptr_t(at)));
+      const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_short4*)(uintptr_t(at)) + 4 / kRows * kPitch / 8);
+      return __builtin_bit_cast(
+          int4v, short8v(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)));
+    }
+  }
+};
+
+// acc += a b with the sums in the accumulation registers.
+template <int TY, int BYTE>
+__device__ inline void mma_acc(float4v& acc, int4v a, int4v b, int sa, int sb) {
+  if constexpr (TY == kGmmBF16)
+    asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+  else if constexpr (TY == kGmmFP16)
+    asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+  else if constexpr (BYTE == 0)
+    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+        : "+a"(acc)
+        : "v"(a), "v"(b), "v"(sa), "v"(sb));
+  else
+    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] "
+        "op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+        : "+a"(acc)
+        : "v"(a), "v"(b), "v"(sa), "v"(sb));
+}
+
+// BM x BN of the output by WM x WN waves, one per SIMD, 128 bytes of the
+// reduction (64 elements of 16 bits, 256 of 4) per stage, through two LDS
+// buffers.  A stage has two halves of 64 bytes.  While a wave multiplies the
+// fragments of one half it reads those of the next into other registers.  Once
+// the second half's are read stands the stage's one barrier: past it nobody
+// reads the stage's buffer again, and the loads of stage s + 2 go there; before
+// it everybody waits for his loads of stage s + 1.
+// Loads past the last stage read zeros.  Every row of every operand begins and
+// ends on a 16-byte chunk, and the rows that a tile reads lie within 4 GiB of
+// its first.
+template <int TY, int MODE, int BM, int BN>
+struct PipeShape {
+  static constexpr int WM = 2, WN = 2, NW = WM * WN;
+  using Q = Layout<MODE != kGmmDw, BM>;   // the operand of the output's rows
+  using C = Layout<MODE == kGmmFwd, BN>;  // the operand of the output's columns
+  static constexpr int kBuf = Q::kBytes + C::kBytes;
+  // Scales: 16 bytes (2 stages) of every row of the tile, two sets; dw: 64
+  // indexes per wave, two sets.
+  static constexpr int kScaleSet = (BM + BN) * 16;
+  static constexpr int kLds =
+      2 * kBuf + (TY == kGmmMX4 ? 2 * kScaleSet : MODE == kGmmDw ? NW * 512 : 0);
+};
+
+template <int TY, int MODE, int BM, int BN>
+__device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds) {
+  using Shape = PipeShape<TY, MODE, BM, BN>;
+  constexpr int WM = Shape::WM, WN = Shape::WN, NW = Shape::NW;
+  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  constexpr bool kColsAlong = MODE == kGmmFwd;
+  constexpr bool kRowsAlong = MODE != kGmmDw;
+  using Q = typename Shape::Q;
+  using C = typename Shape::C;
+  constexpr int kStage = TY == kGmmMX4 ? 256 : 64;
+  constexpr int kPerChunk = kStage / 8;
+  constexpr int kBuf = Shape::kBuf;
+  constexpr int kQ = Q::kLoads / NW, kC = C::kLoads / NW;  // loads per wave and stage
+  static_assert(Q::kLoads % NW == 0 && C::kLoads % NW == 0, "whole wave loads");
+  constexpr bool kGather = MODE == kGmmDw;
+  constexpr bool kScales = TY == kGmmMX4;
+  constexpr int kScaleSet = Shape::kScaleSet;
+  constexpr int kIndexes = kGather ? kC * C::kRows : 64;  // dw: rows of x per wave and stage
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int g = lane >> 4, l16 = lane & 15;
+
+  const int rm = __builtin_amdgcn_readfirstlane(t.rm);
+  const int cn = __builtin_amdgcn_readfirstlane(t.cn);
+  const int red = __builtin_amdgcn_readfirstlane(MODE == kGmmDw ? t.span.m
+                                                 : MODE == kGmmFwd ? p.K : p.N);
+  const int stages = (red + kStage - 1) / kStage;
+  const int64_t e_rows = int64_t(t.span.e) * p.N;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(g_zeros);
+  bool bad_row = false;
+
+  // ---- Where each chunk of this lane begins: base + offset, moved on by a
+  // uniform step per stage.  Outputs past the tile's edge read a row or chunk
+  // inside it: they are not stored.
+  const uint8_t* qbase;
+  const uint8_t* cbase;
+  uint32_t qo[kQ], co[kC];
+  const int64_t qstep = kRowsAlong ? 128 : 64 * p.row_stride;
+  const int64_t cstep = kColsAlong ? 128 : kGather ? 0 : 64 * p.other_stride;
+  if constexpr (kRowsAlong) {
+    qbase = p.rows + (MODE == kGmmFwd && p.index ? 0 : t.span.row0 * p.row_stride);
 #pragma unroll
-  for (int a = 0; a < FM; ++a) {
-    const int r = wm * TM + a * 16 + l16;
-    if (r >= rm) continue;
+    for (int i = 0; i < kQ; ++i) {
+      int r = (wave * kQ + i) * Q::kRows + Q::row(lane);
+      r = r < rm ? r : rm - 1;
+      uint32_t row = uint32_t(r);
+      if (MODE == kGmmFwd && p.index) {
+        const int64_t x = p.index[t.span.row0 + r];
+        const bool ok = x >= 0 && x < p.x_rows;
+        bad_row = bad_row || !ok;
+        row = ok ? uint32_t(x) : 0xffffffffu;
+      }
+      qo[i] = row == 0xffffffffu ? row : row * uint32_t(p.row_stride) + Q::chunk(lane) * 16;
+    }
+  } else {
+    qbase = p.rows + t.span.row0 * p.row_stride + t.out_row0 * 2;
 #pragma unroll
-    for (int d = 0; d < FN; ++d) {
-      const int col = wn * TN + d * 16 + g * 4;
-      if (col >= cn) continue;
-      const int64_t at = (out_first + r) * p.out_stride + c0 + col;
-      const float4v v = acc[a][d];
-      const bool whole = wide && col + 4 <= cn;
-      if (p.out_type == A2AV_FP32) {
-        float* o = reinterpret_cast<float*>(p.out) + at;
-        if (whole)
-          *reinterpret_cast<float4v*>(o) = v;
-        else
-          for (int i = 0; i < 4 && col + i < cn; ++i) o[i] = v[i];
+    for (int i = 0; i < kQ; ++i) {
+      const int ch = Q::chunk(lane);
+      qo[i] = uint32_t((wave * kQ + i) * Q::kRows + Q::row(lane)) * uint32_t(p.row_stride) +
+              (ch * 8 < rm ? ch * 16 : 0);
+    }
+  }
+  if constexpr (kColsAlong) {
+    cbase = p.other + (e_rows + t.c0) * p.other_stride;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int r = (wave * kC + i) * C::kRows + C::row(lane);
+      co[i] = uint32_t(r < cn ? r : cn - 1) * uint32_t(p.other_stride) + C::chunk(lane) * 16;
+    }
+  } else {
+    cbase = p.other + (MODE == kGmmDx ? e_rows * p.other_stride : 0) + t.c0 * 2;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int ch = C::chunk(lane);
+      co[i] = ch * 8 < cn ? ch * 16 : 0;
+      if (MODE == kGmmDx)
+        co[i] += uint32_t((wave * kC + i) * C::kRows + C::row(lane)) * uint32_t(p.other_stride);
+    }
+  }
+  qbase = uniform(qbase);
+  cbase = uniform(cbase);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(uint32_t(uintptr_t((lds_u8*)lds)));
+  const uint32_t extra0 = lds0 + 2 * kBuf;
+
+  // ---- dw: the rows of x.  Each wave keeps the indexes of its own chunks'
+  // rows for kSet stages in LDS, two sets: entry (stage, load, row of the load).
+  constexpr int kSet = 64 / kIndexes;
+  int next_row[kGather ? kC : 1];
+  auto index_row = [&](int s, int at) { return s * 64 + wave * kIndexes + at; };
+  auto load_index = [&](int s) {  // the kSet stages from s (a multiple) on
+    if constexpr (kGather) {
+      const int r = index_row(s + lane / kIndexes, lane % kIndexes);
+      const void* src = r < red ? static_cast<const void*>(p.index + t.span.row0 + r)
+                                : static_cast<const void*>(zeros);
+      load_word_to_lds(src, extra0 + wave * 512 + (s & kSet) * kIndexes * 4);
+    }
+  };
+  auto read_rows = [&](int s) {  // for the loads of stage s
+    if constexpr (kGather) {
+      const int r = C::row(lane);
+      if (p.index) {
+        const uint32_t at = extra0 + wave * 512 + ((s & (2 * kSet - 1)) * kIndexes + r) * 4;
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+          next_row[i] =
+              ((const __attribute__((address_space(3))) int*)(uintptr_t(at)))[i * C::kRows];
       } else {
-        uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
-        uint16_t h[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = round16(v[i], p.out_type);
-        if (whole)
-          *reinterpret_cast<uint64_t*>(o) = __builtin_bit_cast(uint64_t, h);
-        else
-          for (int i = 0; i < 4 && col + i < cn; ++i) o[i] = h[i];
+        for (int i = 0; i < kC; ++i)
+          next_row[i] = int(t.span.row0) + index_row(s, i * C::kRows + r);
+      }
+    }
+  };
+  if constexpr (kGather) {
+    if (p.index)  // a look at all of them, so that the loads need none
+      for (int s = 0; s < stages; s += kSet) {
+        const int r = index_row(s + lane / kIndexes, lane % kIndexes);
+        const int x = r < red ? p.index[t.span.row0 + r] : 0;
+        bad_row = bad_row || (r < red && (x < 0 || x >= p.x_rows));
+      }
+  }
+  // A wave that names a row outside x takes the careful loads throughout.
+  const bool careful = __ballot(bad_row) != 0;
+
+  // ---- scales: a thread brings 16 bytes of a row of the tile (rows operand
+  // first) for two stages.
+  constexpr int kS = kScales ? (BM + BN) / (NW * 64) : 1;
+  const uint8_t* sp[kS];
+  if constexpr (kScales) {
+    static_assert((BM + BN) % (NW * 64) == 0, "whole wave loads of scales");
+#pragma unroll
+    for (int i = 0; i < kS; ++i) {
+      const int r = i * NW * 64 + tid;
+      if (r < BM) {
+        int64_t row = t.span.row0 + (r < rm ? r : rm - 1);
+        if (p.index) row = p.index[row];
+        sp[i] = row >= 0 && row < p.x_rows ? p.row_scales + row * p.blocks : nullptr;
+      } else {
+        sp[i] = p.other_scales + (e_rows + t.c0 + (r - BM < cn ? r - BM : cn - 1)) * p.blocks;
       }
     }
   }
+  auto load_scales = [&](int s) {  // of the stages s and s + 1, s even
+    if constexpr (kScales) {
+#pragma unroll
+      for (int i = 0; i < kS; ++i)
+        load_to_lds(s < stages && sp[i] ? sp[i] + s * 8 : zeros,
+                    extra0 + (s >> 1 & 1) * kScaleSet + (i * NW + wave) * 1024);
+    }
+  };
+
+  // ---- load i of stage s, into buffer s % 2.  FAST: all of it exists.
+  auto load_one = [&](int s, int i, auto fast) {
+    const bool is_q = i < kQ;
+    const uint32_t to = lds0 + (s & 1) * kBuf +
+                        (is_q ? (wave * kQ + i) * Q::kPitch
+                              : Q::kBytes + (wave * kC + i - kQ) * C::kPitch);
+    if (is_q) {
+      const uint8_t* from = qbase + s * qstep;
+      if constexpr (decltype(fast)::value) {
+        load_to_lds(from, qo[i], to);
+      } else {
+        const int at = kRowsAlong ? s * kStage + Q::chunk(lane) * kPerChunk
+                                  : s * 64 + (wave * kQ + i) * Q::kRows + Q::row(lane);
+        load_to_lds(at < red && qo[i] != 0xffffffffu ? from + qo[i] : zeros, to);
+      }
+    } else {
+      const int j = i - kQ;
+      const uint8_t* from = cbase + s * cstep;
+      uint32_t offset = co[j];
+      if constexpr (kGather) offset += uint32_t(next_row[j]) * uint32_t(p.other_stride);
+      if constexpr (decltype(fast)::value) {
+        load_to_lds(from, offset, to);
+      } else {
+        const int at = kColsAlong ? s * kStage + C::chunk(lane) * kPerChunk
+                                  : s * 64 + (wave * kC + j) * C::kRows + C::row(lane);
+        const bool have =
+            at < red && (!kGather || (next_row[j] >= 0 && next_row[j] < p.x_rows));
+        load_to_lds(have ? from + offset : zeros, to);
+      }
+    }
+  };
+  constexpr auto kFast = std::true_type{};
+  constexpr auto kCareful = std::false_type{};
+
+  float4v acc[FM][FN];
+#pragma unroll
+  for (int a = 0; a < FM; ++a)
+#pragma unroll
+    for (int b = 0; b < FN; ++b) acc[a][b] = float4v{0, 0, 0, 0};
+
+  // Fragments of 16 outputs x 64 bytes, one set per half, and their scales (the
+  // bytes of both halves).
+  int4v fq[2][FM], fc[2][FN];
+  int sq[2][kScales ? FM : 1] = {}, sc[2][kScales ? FN : 1] = {};
+  uint32_t q_lane[2], c_lane[2];
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    q_lane[kk] = lds0 + Q::template read_at<kScales>(lane, kk) + wm * FM * Q::kFragment;
+    c_lane[kk] = lds0 + Q::kBytes + C::template read_at<kScales>(lane, kk) + wn * FN * C::kFragment;
+  }
+  const uint32_t s_lane = extra0 + l16 * 16 + g * 2;
+  // Reads fragment f (columns' first) of half kk, and its scale.
+  auto read_one = [&](int kk, int f, uint32_t qa, uint32_t ca, uint32_t sa) {
+    if (f < FN) {
+      fc[kk][f] = C::read(ca + f * C::kFragment);
+      if constexpr (kScales)
+        sc[kk][f] = *((const lds_u16*)(uintptr_t(sa)) + (BM + wn * TN + f * 16) * 8);
+    } else {
+      fq[kk][f - FN] = Q::read(qa + (f - FN) * Q::kFragment);
+      if constexpr (kScales)
+        sq[kk][f - FN] = *((const lds_u16*)(uintptr_t(sa)) + (wm * TM + (f - FN) * 16) * 8);
+    }
+  };
+
+  if (kGather && p.index) {
+    load_index(0);
+    wait_loads<0>();
+  }
+  load_scales(0);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    read_rows(s);
+#pragma unroll
+    for (int i = 0; i < kQ + kC; ++i) load_one(s, i, kCareful);
+  }
+  read_rows(2);
+  wait_loads<kQ + kC>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int f = 0; f < FN + FM; ++f) read_one(0, f, q_lane[0], c_lane[0], s_lane);
+
+  // Products of the two halves, numbered through; the reads of the second
+  // half's fragments, the barrier, the loads and the reads of the next stage's
+  // first half are spread between them.  One wave load occupies the path to
+  // LDS for 16 cycles, as long as a product: 4 waves keep below its rate with
+  // one load per 5 products.
+  constexpr int kHalf = FM * FN, kReads = FM + FN, kAll = kQ + kC;
+  constexpr int kBarrier = kHalf / 2;
+  auto products = [&](int s, auto which, auto fast) {
+    constexpr int kk = decltype(which)::value;
+    const uint32_t buf = ((s + kk) & 1) * kBuf;  // of the fragments to read, half kk ^ 1
+    uint32_t qa = q_lane[kk ^ 1] + buf, ca = c_lane[kk ^ 1] + buf;
+    uint32_t sa =
+        kScales ? s_lane + ((s + kk) >> 1 & 1) * kScaleSet + ((s + kk) & 1) * 8 : 0;
+    // One address register per operand; the fragments are offsets in the
+    // instructions.
+    asm("" : "+v"(qa), "+v"(ca), "+v"(sa));
+    // Whatever the compiler does to the fragments' registers is done before
+    // the first product, with the distance that products need.
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      asm volatile("" : "+v"(fc[kk][f]));
+      if constexpr (kScales) asm volatile("" : "+v"(sc[kk][f]));
+    }
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      asm volatile("" : "+v"(fq[kk][f]));
+      if constexpr (kScales) asm volatile("" : "+v"(sq[kk][f]));
+    }
+    asm volatile("s_nop 1");
+    __builtin_amdgcn_sched_barrier(0);
+    // The compiler would gather the products and put each read right before
+    // its use: it keeps this order.
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+#pragma unroll
+      for (int b = 0; b < FN; ++b) {
+        const int n = a * FN + b, m = kk * kHalf + n;
+        mma_acc<TY, kk>(acc[a][b], fc[kk][b], fq[kk][a], sc[kk][kScales ? b : 0],
+                        sq[kk][kScales ? a : 0]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int r = 0; r < kReads; ++r)
+          if (n == (kk == 0 ? r * (kBarrier * 3 / 4) / kReads : r * (kHalf * 3 / 4) / kReads)) {
+            read_one(kk ^ 1, r, qa, ca, sa);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        if (m == kBarrier - 1) {
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          if constexpr (kScales) {
+            if ((s & 1) == 0) load_scales(s + 2);
+          }
+          if constexpr (kGather) {
+            if (p.index && (s & (kSet - 1)) == 0) load_index(s + kSet);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < kAll; ++i)
+          if (m == kBarrier + i * (kHalf * 5 / 4) / kAll) {
+            load_one(s + 2, i, fast);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+      }
+    }
+  };
+  auto stage = [&](int s, auto fast) {
+    products(s, std::integral_constant<int, 0>{}, fast);
+    products(s, std::integral_constant<int, 1>{}, fast);
+    read_rows(s + 3);
+  };
+  int s = 0;
+  if (!careful)
+    for (; (s + 3) * kStage <= red; ++s) stage(s, kFast);
+  for (; s < stages; ++s) stage(s, kCareful);
+  // The loads still in flight write to this workgroup's LDS; the last products
+  // have to end before their sums are read.
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int a = 0; a < FM; ++a)
+#pragma unroll
+    for (int b = 0; b < FN; ++b) asm volatile("" : "+a"(acc[a][b]));
+  if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
+  __syncthreads();  // everybody's reads and loads are done
+  constexpr int kPart = 2 * kBuf / NW / 1024 * 1024;
+  if (p.out_type == A2AV_FP32)
+    store_rows<MODE, TM, TN, FM, FN, 4>(p, t, acc, wm, wn, lds + wave * kPart, kPart);
+  else
+    store_rows<MODE, TM, TN, FM, FN, 2>(p, t, acc, wm, wn, lds + wave * kPart, kPart);
 }
 
-template <int TY, int MODE, int BM, int BN, int WM, int WN, bool DIRECT>
-hipError_t launch_tiles(const GmmParams& p, hipStream_t stream) {
+// 256 x 256 tiles, one workgroup per CU.
+template <int TY, int MODE>
+__global__ __launch_bounds__(256, 1) void gmm_large(const GmmParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[PipeShape<TY, MODE, 256, 256>::kLds];
+  Tile t;
+  int part;
+  if (!find_work<MODE, 256, 256, true>(p, &t, &part)) return;
+  if (part < 0)
+    gmm_tile<TY, MODE, 256, 256>(p, t, lds);
+  else
+    gmm_tile<TY, MODE, 128, 128>(p, t, lds);
+}
+
+// 128 x 128 tiles, two workgroups per CU.
+template <int TY, int MODE>
+__global__ __launch_bounds__(256, 2) void gmm_small(const GmmParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[PipeShape<TY, MODE, 128, 128>::kLds];
+  Tile t;
+  int part;
+  if (!find_work<MODE, 128, 128, false>(p, &t, &part)) return;
+  gmm_tile<TY, MODE, 128, 128>(p, t, lds);
+}
+
+// Launches `kernel` over the tiles that the counts can need: they stay on the
+// device, so as many row tiles as there can be.
+template <int MODE, int BM, int BN, class Kernel>
+hipError_t launch_tiles(Kernel kernel, int threads, const GmmParams& p, hipStream_t stream) {
   const int64_t cols = MODE == kGmmFwd ? p.N : p.K;
   const int64_t col_tiles = (cols + BN - 1) / BN;
-  // The counts stay on the device: as many row tiles as they can need.
   const int64_t used = p.E < p.nrows ? p.E : p.nrows;
   const int64_t row_tiles = MODE == kGmmDw ? int64_t(p.E) * ((p.N + BM - 1) / BM)
                                            : (p.nrows + used * (BM - 1)) / BM;
-  const int64_t grid = (row_tiles * col_tiles + 7) / 8 * 8;
-  if (grid <= 0) return hipSuccess;
+  if (row_tiles * col_tiles <= 0) return hipSuccess;
+  // Quarters of up to 128 tiles come on top.
+  const int64_t grid = (row_tiles * col_tiles + (BM == 256 ? 3 * 128 : 0) + 7) / 8 * 8;
   // A launch's threads have to stay below 2^32 in x: long ones go on in y.
   const int64_t gx = grid < (1 << 20) ? grid : (1 << 20);
   const int64_t gy = (grid + gx - 1) / gx;
   if (gy > 65535) return hipErrorInvalidConfiguration;
   (void)hipGetLastError();
-  gmm_kernel<TY, MODE, BM, BN, WM, WN, DIRECT>
-      <<<dim3(uint32_t(gx), uint32_t(gy)), dim3(WM * WN * 64), 0, stream>>>(p);
+  kernel<<<dim3(uint32_t(gx), uint32_t(gy)), dim3(uint32_t(threads)), 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <int TY, int MODE>
 hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
-  if constexpr (TY == kGmmMX4) {
-    (void)direct;
-    return launch_tiles<TY, MODE, 128, 128, 2, 2, true>(p, stream);
-  } else {
-    if (direct) return launch_tiles<TY, MODE, 128, 128, 2, 2, true>(p, stream);
-    return launch_tiles<TY, MODE, 128, 128, 2, 2, false>(p, stream);
+  if (direct) {
+    // Rows of an expert (dw: of the reduction, which no tile cuts).
+    const bool large = MODE == kGmmDw || p.nrows / p.E >= 160;
+    if (large) return launch_tiles<MODE, 256, 256>(gmm_large<TY, MODE>, 256, p, stream);
+    return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE>, 256, p, stream);
   }
+  return launch_tiles<MODE, 128, 128>(gmm_kernel<TY, MODE, 128, 128, 2, 2, TY == kGmmMX4>, 256, p,
+                                      stream);
 }
 
 }  // namespace
@@ -538,9 +1137,19 @@ hipError_t launch_gmm(const GmmParams& p, GmmType type, GmmMode mode, hipStream_
   // The loads to LDS move aligned chunks of 16 bytes: every row has to begin
   // and end on one.
   const uintptr_t bases = reinterpret_cast<uintptr_t>(p.rows) | reinterpret_cast<uintptr_t>(p.other);
+  // They go by 32-bit offsets from a tile's first row (x that is gathered: from
+  // its first).  Anything else takes the kernel with plain loads.
+  const int64_t far = (int64_t(1) << 32) - 256;
+  const bool all_x = mode == kGmmDw || (mode == kGmmFwd && p.index);
+  const int64_t x_stride = mode == kGmmDw ? p.other_stride : p.row_stride;
   const bool direct = ((bases | uint64_t(p.row_stride) | uint64_t(p.other_stride)) & 15) == 0 &&
-                      ((p.N | p.K) & 7) == 0;
-  if (type == kGmmMX4) return launch_mode<kGmmMX4, kGmmFwd>(p, true, stream);
+                      ((p.N | p.K) & 7) == 0 && p.row_stride <= far / 256 &&
+                      p.other_stride <= far / 256 && (!all_x || x_stride <= far / (p.x_rows + 1));
+  if (type == kGmmMX4) {
+    const uintptr_t scales = reinterpret_cast<uintptr_t>(p.row_scales) |
+                             reinterpret_cast<uintptr_t>(p.other_scales) | uintptr_t(p.blocks);
+    return launch_mode<kGmmMX4, kGmmFwd>(p, direct && scales % 16 == 0, stream);
+  }
   if (type == kGmmBF16) {
     if (mode == kGmmFwd) return launch_mode<kGmmBF16, kGmmFwd>(p, direct, stream);
     if (mode == kGmmDx) return launch_mode<kGmmBF16, kGmmDx>(p, direct, stream);

@@ -208,3 +208,28 @@ def test_another_stream_and_graph():
         torch.cuda.synchronize()
         want = [moe.gmm(x, w, c), moe.gmm_dx(dy, w, c), moe.gmm_dw(dy, x, c)]
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("counts,N,K", [([520, 300], 16640, 136), ([1100, 0, 3], 2048, 16640),
+                                        ([700, 90], 1000, 8456), ([5000], 4096, 264)])
+def test_rounds_of_whole_tiles_and_cut_ones(counts, N, K):
+    """More tiles than CUs, in one direction or another, and a part of a round."""
+    check_all(torch.Generator().manual_seed(N), counts, N, K, torch.bfloat16)
+
+
+@pytest.mark.parametrize("K", [64, 128, 192, 256, 320, 72, 200])
+def test_lengths_around_the_stages(K):
+    gen = torch.Generator().manual_seed(K)
+    check_all(gen, [200, 0, 310], 264, K, torch.float16)
+    check_all(gen, [K, 3 * K, 1, 2], 136, 264, torch.bfloat16, tokens=50)
+
+
+def test_far_rows_take_the_plain_loads():
+    """A stride of which 256 rows pass 4 GiB: the same values as close together."""
+    gen = torch.Generator().manual_seed(8)
+    x, w, dy, c = make(gen, 3, 1, 64, 128, torch.bfloat16, [3])
+    far = torch.empty(2 ** 24 * 2 + 128, dtype=torch.bfloat16, device=DEV)
+    xf = far.as_strided((3, 128), (2 ** 24, 1))
+    xf.copy_(x)
+    assert torch.equal(moe.gmm(xf, w, c), moe.gmm(x, w, c))
+    assert torch.equal(moe.gmm_dw(dy, xf, c), moe.gmm_dw(dy, x, c))

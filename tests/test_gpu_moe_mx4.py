@@ -105,6 +105,17 @@ def test_product(dt, counts, N, K):
     product(counts, N, K, dt, seed=N + K)
 
 
+@pytest.mark.parametrize("K", [512, 1024, 1536, 2560])
+@pytest.mark.parametrize("counts,N,tokens", [([300, 0, 200], 520, None), ([40, 3, 0, 77], 130, 90),
+                                             ([2, 1], 48, None)])
+def test_product_of_whole_scale_groups(counts, N, K, tokens):
+    product(counts, N, K, torch.bfloat16, tokens, seed=K + N)
+
+
+def test_product_in_rounds_of_whole_tiles():
+    product([520, 300], 16640, 512, torch.float16, seed=3)
+
+
 @pytest.mark.parametrize("counts,N,K,tokens", [([9, 0, 30], 64, 256, 11), ([200, 77], 200, 416, 100)])
 def test_product_of_gathered_rows(counts, N, K, tokens):
     product(counts, N, K, torch.bfloat16, tokens, seed=tokens)
