@@ -734,22 +734,23 @@ __device__ inline void mma_acc(float4v& acc, int4v a, int4v b, int sa, int sb) {
 // Loads past the last stage read zeros.  Every row of every operand begins and
 // ends on a 16-byte chunk, and the rows that a tile reads lie within 4 GiB of
 // its first.
-template <int TY, int MODE, int BM, int BN>
+template <int TY, int MODE, int BM, int BN, int NB>
 struct PipeShape {
   static constexpr int WM = 2, WN = 2, NW = WM * WN;
   using Q = Layout<MODE != kGmmDw, BM>;   // the operand of the output's rows
   using C = Layout<MODE == kGmmFwd, BN>;  // the operand of the output's columns
   static constexpr int kBuf = Q::kBytes + C::kBytes;
-  // Scales: 16 bytes (2 stages) of every row of the tile, two sets; dw: 64
-  // indexes per wave, two sets.
-  static constexpr int kScaleSet = (BM + BN) * 16;
+  // Scales: 16 bytes (2 stages) of every row of the tile, as many sets
+  // as the buffers' stages span; dw: 64
+  // indexes per wave, four sets.
+  static constexpr int kScaleSet = (BM + BN) * 16, kScaleSets = NB / 2 + 1;
   static constexpr int kLds =
-      2 * kBuf + (TY == kGmmMX4 ? 2 * kScaleSet : MODE == kGmmDw ? NW * 512 : 0);
+      NB * kBuf + (TY == kGmmMX4 ? kScaleSets * kScaleSet : MODE == kGmmDw ? NW * 1024 : 0);
 };
 
-template <int TY, int MODE, int BM, int BN>
+template <int TY, int MODE, int BM, int BN, int NB>
 __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds) {
-  using Shape = PipeShape<TY, MODE, BM, BN>;
+  using Shape = PipeShape<TY, MODE, BM, BN, NB>;
   constexpr int WM = Shape::WM, WN = Shape::WN, NW = Shape::NW;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool kColsAlong = MODE == kGmmFwd;
@@ -832,11 +833,14 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
   qbase = uniform(qbase);
   cbase = uniform(cbase);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(uint32_t(uintptr_t((lds_u8*)lds)));
-  const uint32_t extra0 = lds0 + 2 * kBuf;
+  const uint32_t extra0 = lds0 + NB * kBuf;
 
   // ---- dw: the rows of x.  Each wave keeps the indexes of its own chunks'
-  // rows for kSet stages in LDS, two sets: entry (stage, load, row of the load).
+  // rows for kSet stages in LDS, four sets: entry (stage, load, row of the load).
+  // A set is loaded at least NB - 1 stages before its first index is read, when
+  // the waits of that many stages have covered it.
   constexpr int kSet = 64 / kIndexes;
+  static_assert(!kGather || (2 * kSet - NB - 1 >= NB - 1 && NB <= 4), "indexes in time");
   int next_row[kGather ? kC : 1];
   auto index_row = [&](int s, int at) { return s * 64 + wave * kIndexes + at; };
   auto load_index = [&](int s) {  // the kSet stages from s (a multiple) on
@@ -844,14 +848,14 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
       const int r = index_row(s + lane / kIndexes, lane % kIndexes);
       const void* src = r < red ? static_cast<const void*>(p.index + t.span.row0 + r)
                                 : static_cast<const void*>(zeros);
-      load_word_to_lds(src, extra0 + wave * 512 + (s & kSet) * kIndexes * 4);
+      load_word_to_lds(src, extra0 + wave * 1024 + (s / kSet & 3) * 256);
     }
   };
   auto read_rows = [&](int s) {  // for the loads of stage s
     if constexpr (kGather) {
       const int r = C::row(lane);
       if (p.index) {
-        const uint32_t at = extra0 + wave * 512 + ((s & (2 * kSet - 1)) * kIndexes + r) * 4;
+        const uint32_t at = extra0 + wave * 1024 + ((s & (4 * kSet - 1)) * kIndexes + r) * 4;
 #pragma unroll
         for (int i = 0; i < kC; ++i)
           next_row[i] =
@@ -897,14 +901,14 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
 #pragma unroll
       for (int i = 0; i < kS; ++i)
         load_to_lds(s < stages && sp[i] ? sp[i] + s * 8 : zeros,
-                    extra0 + (s >> 1 & 1) * kScaleSet + (i * NW + wave) * 1024);
+                    extra0 + (s >> 1) % Shape::kScaleSets * kScaleSet + (i * NW + wave) * 1024);
     }
   };
 
   // ---- load i of stage s, into buffer s % 2.  FAST: all of it exists.
   auto load_one = [&](int s, int i, auto fast) {
     const bool is_q = i < kQ;
-    const uint32_t to = lds0 + (s & 1) * kBuf +
+    const uint32_t to = lds0 + s % NB * kBuf +
                         (is_q ? (wave * kQ + i) * Q::kPitch
                               : Q::kBytes + (wave * kC + i - kQ) * C::kPitch);
     if (is_q) {
@@ -967,17 +971,19 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
 
   if (kGather && p.index) {
     load_index(0);
+    load_index(kSet);
     wait_loads<0>();
   }
-  load_scales(0);
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < NB; s += 2) load_scales(s);
+#pragma unroll
+  for (int s = 0; s < NB; ++s) {
     read_rows(s);
 #pragma unroll
     for (int i = 0; i < kQ + kC; ++i) load_one(s, i, kCareful);
   }
-  read_rows(2);
-  wait_loads<kQ + kC>();
+  read_rows(NB);
+  wait_loads<(NB - 1) * (kQ + kC)>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 #pragma unroll
@@ -992,10 +998,10 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
   constexpr int kBarrier = kHalf / 2;
   auto products = [&](int s, auto which, auto fast) {
     constexpr int kk = decltype(which)::value;
-    const uint32_t buf = ((s + kk) & 1) * kBuf;  // of the fragments to read, half kk ^ 1
+    const uint32_t buf = (s + kk) % NB * kBuf;  // of the fragments to read, half kk ^ 1
     uint32_t qa = q_lane[kk ^ 1] + buf, ca = c_lane[kk ^ 1] + buf;
     uint32_t sa =
-        kScales ? s_lane + ((s + kk) >> 1 & 1) * kScaleSet + ((s + kk) & 1) * 8 : 0;
+        kScales ? s_lane + ((s + kk) >> 1) % Shape::kScaleSets * kScaleSet + ((s + kk) & 1) * 8 : 0;
     // One address register per operand; the fragments are offsets in the
     // instructions.
     asm("" : "+v"(qa), "+v"(ca), "+v"(sa));
@@ -1030,21 +1036,22 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
             __builtin_amdgcn_sched_barrier(0);
           }
         if (m == kBarrier - 1) {
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+          // The loads of stage s + 1 and all before them have arrived.
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NB - 2) * kAll) : "memory");
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
           if constexpr (kScales) {
-            if ((s & 1) == 0) load_scales(s + 2);
+            if ((s & 1) == 0) load_scales(s + NB);
           }
           if constexpr (kGather) {
-            if (p.index && (s & (kSet - 1)) == 0) load_index(s + kSet);
+            if (p.index && (s & (kSet - 1)) == 0) load_index(s + 2 * kSet);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int i = 0; i < kAll; ++i)
           if (m == kBarrier + i * (kHalf * 5 / 4) / kAll) {
-            load_one(s + 2, i, fast);
+            load_one(s + NB, i, fast);
             __builtin_amdgcn_sched_barrier(0);
           }
       }
@@ -1053,11 +1060,11 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
   auto stage = [&](int s, auto fast) {
     products(s, std::integral_constant<int, 0>{}, fast);
     products(s, std::integral_constant<int, 1>{}, fast);
-    read_rows(s + 3);
+    read_rows(s + NB + 1);
   };
   int s = 0;
   if (!careful)
-    for (; (s + 3) * kStage <= red; ++s) stage(s, kFast);
+    for (; (s + NB + 1) * kStage <= red; ++s) stage(s, kFast);
   for (; s < stages; ++s) stage(s, kCareful);
   // The loads still in flight write to this workgroup's LDS; the last products
   // have to end before their sums are read.
@@ -1068,7 +1075,7 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
     for (int b = 0; b < FN; ++b) asm volatile("" : "+a"(acc[a][b]));
   if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
   __syncthreads();  // everybody's reads and loads are done
-  constexpr int kPart = 2 * kBuf / NW / 1024 * 1024;
+  constexpr int kPart = NB * kBuf / NW / 1024 * 1024;
   if (p.out_type == A2AV_FP32)
     store_rows<MODE, TM, TN, FM, FN, 4>(p, t, acc, wm, wn, lds + wave * kPart, kPart);
   else
@@ -1078,24 +1085,148 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
 // 256 x 256 tiles, one workgroup per CU.
 template <int TY, int MODE>
 __global__ __launch_bounds__(256, 1) void gmm_large(const GmmParams p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[PipeShape<TY, MODE, 256, 256>::kLds];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[PipeShape<TY, MODE, 256, 256, 2>::kLds];
+  static_assert(PipeShape<TY, MODE, 128, 128, 4>::kLds <= sizeof(lds), "quarters fit");
   Tile t;
   int part;
   if (!find_work<MODE, 256, 256, true>(p, &t, &part)) return;
   if (part < 0)
-    gmm_tile<TY, MODE, 256, 256>(p, t, lds);
+    gmm_tile<TY, MODE, 256, 256, 2>(p, t, lds);
   else
-    gmm_tile<TY, MODE, 128, 128>(p, t, lds);
+    gmm_tile<TY, MODE, 128, 128, 4>(p, t, lds);
 }
 
 // 128 x 128 tiles, two workgroups per CU.
-template <int TY, int MODE>
-__global__ __launch_bounds__(256, 2) void gmm_small(const GmmParams p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[PipeShape<TY, MODE, 128, 128>::kLds];
+template <int TY, int MODE, int NB>
+__global__ __launch_bounds__(256, NB == 2 ? 2 : 1) void gmm_small(const GmmParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[PipeShape<TY, MODE, 128, 128, NB>::kLds];
   Tile t;
   int part;
   if (!find_work<MODE, 128, 128, false>(p, &t, &part)) return;
-  gmm_tile<TY, MODE, 128, 128>(p, t, lds);
+  gmm_tile<TY, MODE, 128, 128, NB>(p, t, lds);
+}
+
+// ------------------------------------------------------------------ few rows per expert
+
+// MT x 16 rows and FN x 16 columns by 8 waves that share out the reduction.
+// With few rows an expert's weight is read for little work, and its bytes are
+// the time: every wave streams its part of W straight into registers (nothing
+// of it is used twice, so LDS would only be a detour), 4 steps of 64 bytes per
+// row at a time, and the waves' sums meet in LDS, in the order of the waves.
+template <int TY, int MT, int FN>
+__global__ __launch_bounds__(512, MT <= 2 ? 4 : 2) void gmm_few(const GmmParams p) {
+  constexpr int NW = 8, BM = MT * 16, BN = FN * 16, U = 4;
+  constexpr int kStep = TY == kGmmMX4 ? 128 : 32;  // reduction elements per product
+  __shared__ float part[NW][MT * FN][64 * 4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int g = lane >> 4, l16 = lane & 15;
+  Tile t;
+  int cut;
+  if (!find_work<kGmmFwd, BM, BN, false>(p, &t, &cut)) return;
+  const int64_t w0 = int64_t(t.span.e) * p.N + t.c0;
+  const int K = p.K;
+  constexpr int kPerChunk = kStep / 4;
+
+  const uint8_t* x[MT];
+  const uint8_t* w[FN];
+  const uint8_t* xs[TY == kGmmMX4 ? MT : 1];
+  const uint8_t* ws[TY == kGmmMX4 ? FN : 1];
+  bool real[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int r = i * 16 + l16;
+    int64_t row = t.span.row0 + (r < t.rm ? r : t.rm - 1);
+    if (p.index) row = p.index[row];
+    real[i] = row >= 0 && row < p.x_rows;
+    if (!real[i] && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
+    x[i] = p.rows + (real[i] ? row : 0) * p.row_stride + g * 16;
+    if constexpr (TY == kGmmMX4) xs[i] = p.row_scales + (real[i] ? row : 0) * p.blocks;
+  }
+#pragma unroll
+  for (int f = 0; f < FN; ++f) {
+    const int c = f * 16 + l16;
+    const int64_t row = w0 + (c < t.cn ? c : t.cn - 1);
+    w[f] = p.other + row * p.other_stride + g * 16;
+    if constexpr (TY == kGmmMX4) ws[f] = p.other_scales + row * p.blocks;
+  }
+  const bool scales4 = TY == kGmmMX4 &&
+                       ((reinterpret_cast<uintptr_t>(p.row_scales) |
+                         reinterpret_cast<uintptr_t>(p.other_scales) | uintptr_t(p.blocks)) & 3) == 0;
+  // The scale of this lane's chunk in step u, in the low byte.
+  auto scale = [&](const uint8_t* at, int step) -> int {
+    if (scales4) return int(reinterpret_cast<const uint32_t*>(at)[step] >> (8 * g));
+    return step * 4 + g < p.blocks ? at[step * 4 + g] : 0x7f;
+  };
+
+  float4v acc[MT][FN];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int f = 0; f < FN; ++f) acc[i][f] = float4v{0, 0, 0, 0};
+
+  // Steps first .. first + n of 64 bytes; TAIL: some may lie past the end.
+  auto run = [&](int first, auto n, auto tail) {
+    constexpr int kN = decltype(n)::value;
+    int4v wv[kN][FN], xv[kN][MT];
+    int wsv[kN][FN], xsv[kN][MT];
+#pragma unroll
+    for (int u = 0; u < kN; ++u) {
+      const bool have =
+          !decltype(tail)::value || (first + u) * kStep + g * kPerChunk < K;
+#pragma unroll
+      for (int f = 0; f < FN; ++f) {
+        wv[u][f] = int4v{0, 0, 0, 0};
+        if (have) wv[u][f] = *reinterpret_cast<const int4v*>(w[f] + int64_t(first + u) * 64);
+        if constexpr (TY == kGmmMX4) wsv[u][f] = have ? scale(ws[f], first + u) : 0x7f;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        xv[u][i] = int4v{0, 0, 0, 0};
+        if (have && real[i])
+          xv[u][i] = *reinterpret_cast<const int4v*>(x[i] + int64_t(first + u) * 64);
+        if constexpr (TY == kGmmMX4) xsv[u][i] = have && real[i] ? scale(xs[i], first + u) : 0x7f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kN; ++u)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+          if constexpr (TY == kGmmMX4)
+            acc[i][f] = mma_mx4(wv[u][f], xv[u][i], acc[i][f], wsv[u][f], xsv[u][i], 0);
+          else
+            acc[i][f] = mma<TY>(wv[u][f], xv[u][i], acc[i][f]);
+        }
+  };
+  // Waves take groups of U steps in turn.
+  const int steps = (K + kStep - 1) / kStep;
+  const int whole = K / kStep / U * U;
+  for (int s = wave * U; s < whole; s += NW * U)
+    run(s, std::integral_constant<int, U>{}, std::false_type{});
+  for (int s = whole + wave; s < steps; s += NW)
+    run(s, std::integral_constant<int, 1>{}, std::true_type{});
+
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+      *reinterpret_cast<float4v*>(&part[wave][i * FN + f][lane * 4]) = acc[i][f];
+  __syncthreads();
+  // Element (r, c): column c % 16 = 4g + j of fragment (r / 16, c / 16), lane 16 g + r % 16.
+  for (int q = tid; q < BM * BN; q += 512) {
+    const int r = q / BN, c = q % BN;
+    if (r >= t.rm || c >= t.cn) continue;
+    const int at = ((c & 15) >> 2) * 64 + (r & 15) * 4 + (c & 3);
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) v += part[i][(r >> 4) * FN + (c >> 4)][at];
+    const int64_t o = (t.out_row0 + r) * p.out_stride + t.c0 + c;
+    if (p.out_type == A2AV_FP32)
+      reinterpret_cast<float*>(p.out)[o] = v;
+    else
+      reinterpret_cast<uint16_t*>(p.out)[o] = round16(v, p.out_type);
+  }
 }
 
 // Launches `kernel` over the tiles that the counts can need: they stay on the
@@ -1121,11 +1252,24 @@ hipError_t launch_tiles(Kernel kernel, int threads, const GmmParams& p, hipStrea
 
 template <int TY, int MODE>
 hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
+  if constexpr (MODE == kGmmFwd) {
+    // By the mean rows of an expert (the counts stay on the device).
+    if (direct && p.nrows <= int64_t(p.E) * 12)
+      return launch_tiles<MODE, 16, 32>(gmm_few<TY, 1, 2>, 512, p, stream);
+    if (direct && p.nrows <= int64_t(p.E) * 40)
+      return launch_tiles<MODE, 32, 32>(gmm_few<TY, 2, 2>, 512, p, stream);
+  }
   if (direct) {
+    const int64_t cols = MODE == kGmmFwd ? p.N : p.K;
+    const int64_t used = p.E < p.nrows ? p.E : p.nrows;
     // Rows of an expert (dw: of the reduction, which no tile cuts).
     const bool large = MODE == kGmmDw || p.nrows / p.E >= 160;
     if (large) return launch_tiles<MODE, 256, 256>(gmm_large<TY, MODE>, 256, p, stream);
-    return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE>, 256, p, stream);
+    // Tiles for every CU: two workgroups on each hide each other's ends.  Fewer:
+    // one, with four stages of loads in flight.
+    if ((p.nrows / 128 + used / 2) * ((cols + 127) / 128) > 384)
+      return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 2>, 256, p, stream);
+    return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 4>, 256, p, stream);
   }
   return launch_tiles<MODE, 128, 128>(gmm_kernel<TY, MODE, 128, 128, 2, 2, TY == kGmmMX4>, 256, p,
                                       stream);
