@@ -1,7 +1,7 @@
 // moe_route.hip -- the top-k router and its gradient.
 //
 // A wave takes a token: its E logits sit in the wave's registers (logit
-// 64 i + lane in register i), the k largest are taken one after the other by
+// PER * lane + i in register i), the k largest are taken one after the other by
 // a maximum over the wave, and the softmax sum is one more reduction.  The
 // slots then have to be put in expert order, stably: a slot's row is
 //   (slots of smaller experts) + (slots of its expert in earlier blocks)
@@ -40,89 +40,210 @@ __device__ inline void store_value(void* p, int64_t i, int dtype, float v) {
     static_cast<uint16_t*>(p)[i] = __builtin_bit_cast(uint16_t, _Float16(v));
 }
 
-// Rising unsigned keys in the order of the logits: 0 for -inf (not to be
-// chosen), NaN on top, both zeros alike.
+// Rising unsigned keys in the order of the logits: NaN on top, both zeros alike,
+// -inf (not to be chosen) at kNoKey.
+constexpr uint32_t kNoKey = 0x007fffffu;
 __device__ inline uint32_t key_of(float v) {
-  v += 0.0f;
-  const uint32_t b = __float_as_uint(v);
-  if (v != v) return 0xffffffffu;
-  if (b == 0xff800000u) return 0;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  const uint32_t key = b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+  return v != v ? 0xffffffffu : key;
+}
+// The logit of a key (any NaN for that of NaN).
+__device__ inline float of_key(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+// Reductions over the wave by lane moves inside rows of 16 lanes and from row to
+// row: the result stands in lane 63.  Six moves of the vector unit; through LDS
+// (shuffles) the same took 2.5 times as long.
+template <class F>
+__device__ inline int wave_reduce(int v, int none, F f) {
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x111, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x112, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x114, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x118, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x142, 0xa, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x143, 0xc, 0xf, false));
+  return v;
 }
 
 __device__ inline uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    const uint32_t u = __shfl_xor(v, d);
-    v = u > v ? u : v;
-  }
-  return v;
+  const auto f = [](int a, int b) { return int(uint32_t(a) > uint32_t(b) ? a : b); };
+  return uint32_t(__builtin_amdgcn_readlane(wave_reduce(int(v), 0, f), 63));
+}
+
+__device__ inline float wave_fmax(float v) {
+  const auto f = [](int a, int b) {
+    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+  };
+  const int none = __float_as_int(-__builtin_inff());
+  return __int_as_float(
+      __builtin_amdgcn_readlane(wave_reduce(__float_as_int(v), none, f), 63));
 }
 
 __device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  const auto f = [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  };
+  return __int_as_float(__builtin_amdgcn_readlane(wave_reduce(__float_as_int(v), 0, f), 63));
 }
 
 __device__ inline int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
+  return wave_reduce(v, 0, [](int a, int b) { return a + b; });
+}
+
+// exp(x), x <= 0 or NaN, within 2 steps: 2^t for t = x log2(e) rounded, times
+// 1 + ln(2) (x log2(e) - t).  Results below the normal numbers are 0.
+__device__ inline float exp_of(float x) {
+  const float t = x * 1.44269504f;
+  const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return x < -150.0f ? 0.0f : fmaf(e, r * 0.693147181f, e);
+}
+
+// A row of E logits: PER of them in a row to a lane, -inf past the end.  VEC:
+// every lane's are one aligned piece of the row or all past its end.
+template <int PER>
+struct Row {
+  float v[PER];
+
+  __device__ void load(const void* p, int64_t at, int E, int dtype, bool vec) {
+    const int e0 = (threadIdx.x & 63) * PER;
+    if (PER > 1 && vec) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    if (lane >= d) v += u;
+      for (int i = 0; i < PER; ++i) v[i] = -__builtin_inff();
+      if (e0 >= E) return;
+      if (dtype == A2AV_FP32) {
+        constexpr int kN = PER < 4 ? PER : 4;
+        typedef float Piece __attribute__((ext_vector_type(kN < 2 ? 2 : kN)));
+#pragma unroll
+        for (int i = 0; i < PER; i += kN) {
+          const Piece w = *reinterpret_cast<const Piece*>(static_cast<const float*>(p) + at + e0 + i);
+#pragma unroll
+          for (int j = 0; j < kN; ++j) v[i + j] = w[j];
+        }
+      } else {
+        constexpr int kN = PER < 8 ? PER : 8;
+        typedef uint16_t Piece __attribute__((ext_vector_type(kN < 2 ? 2 : kN)));
+#pragma unroll
+        for (int i = 0; i < PER; i += kN) {
+          const Piece w =
+              *reinterpret_cast<const Piece*>(static_cast<const uint16_t*>(p) + at + e0 + i);
+#pragma unroll
+          for (int j = 0; j < kN; ++j)
+            v[i + j] = dtype == A2AV_BF16 ? __uint_as_float(uint32_t(w[j]) << 16)
+                                          : float(__builtin_bit_cast(_Float16, uint16_t(w[j])));
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      v[i] = e0 + i < E ? load_value(p, at + e0 + i, dtype) : -__builtin_inff();
   }
-  return v;
+
+  // dtype's rounding of x, contiguous from p[at] on.
+  __device__ static void store(void* p, int64_t at, int E, int dtype, bool vec,
+                               const float (&x)[PER]) {
+    const int e0 = (threadIdx.x & 63) * PER;
+    if (PER > 1 && vec) {
+      if (e0 >= E) return;
+      if (dtype == A2AV_FP32) {
+        constexpr int kN = PER < 4 ? PER : 4;
+        typedef float Piece __attribute__((ext_vector_type(kN < 2 ? 2 : kN)));
+#pragma unroll
+        for (int i = 0; i < PER; i += kN) {
+          Piece w;
+#pragma unroll
+          for (int j = 0; j < kN; ++j) w[j] = x[i + j];
+          *reinterpret_cast<Piece*>(static_cast<float*>(p) + at + e0 + i) = w;
+        }
+      } else {
+        constexpr int kN = PER < 8 ? PER : 8;
+        typedef uint16_t Piece __attribute__((ext_vector_type(kN < 2 ? 2 : kN)));
+#pragma unroll
+        for (int i = 0; i < PER; i += kN) {
+          Piece w;
+#pragma unroll
+          for (int j = 0; j < kN; ++j)
+            w[j] = dtype == A2AV_BF16 ? __builtin_bit_cast(uint16_t, __bf16(x[i + j]))
+                                      : __builtin_bit_cast(uint16_t, _Float16(x[i + j]));
+          *reinterpret_cast<Piece*>(static_cast<uint16_t*>(p) + at + e0 + i) = w;
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e0 + i < E) store_value(p, at + e0 + i, dtype, x[i]);
+  }
+};
+
+// Whether rows of E logits from p on, `stride` apart, are whole pieces.
+template <int PER>
+__device__ inline bool row_pieces(const void* p, int64_t stride, int E, int dtype) {
+  const int size = dtype == A2AV_FP32 ? 4 : 2;
+  const int piece = PER * size < 16 ? PER * size : 16;
+  return E % PER == 0 && (stride * size) % piece == 0 &&
+         reinterpret_cast<uintptr_t>(p) % uintptr_t(piece) == 0;
 }
 
 // One token by one wave: writes experts and weights, and the experts to LDS.
 template <int PER>
-__device__ inline void choose(const RouteParams& p, int t, int32_t* ids) {
+__device__ inline void choose(const RouteParams& p, int t, const float (&v)[PER], int32_t* ids) {
   const int lane = threadIdx.x & 63;
-  float v[PER];
+  // Each lane's keys in falling order, equal ones in their own (neighbours
+  // change places only when out of order), and which logits they were, 4 bits
+  // each: the choice below looks at first keys alone.
   uint32_t key[PER];
-  const int64_t at = int64_t(t) * p.stride;
+  int id[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = i * 64 + lane;
-    v[i] = e < p.E ? load_value(p.logits, at + e, p.dtype) : -__builtin_inff();
+    key[i] = key_of(v[i]);
+    id[i] = i;
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) key[i] = key_of(v[i]);
-
-  float most = 0.0f, picked = 0.0f;  // picked: lane j holds slot j
-  int mine = -1;
-  for (int j = 0; j < p.k; ++j) {
-    uint32_t m = key[0];
+  for (int n = 1; n < PER; ++n)
 #pragma unroll
-    for (int i = 1; i < PER; ++i) m = key[i] > m ? key[i] : m;
-    m = wave_max(m);
-    if (m == 0) break;
-    int e = -1;
-    float val = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const uint64_t at_i = __ballot(key[i] == m);
-      if (e < 0 && at_i) {
-        const int l = __ffsll((unsigned long long)at_i) - 1;
-        e = i * 64 + l;
-        val = __shfl(v[i], l);
-        if (lane == l) key[i] = 0;
-      }
+    for (int i = n; i > 0; --i) {
+      const bool swap = key[i] > key[i - 1];
+      const uint32_t hi = swap ? key[i] : key[i - 1], lo = swap ? key[i - 1] : key[i];
+      const int hi_id = swap ? id[i] : id[i - 1], lo_id = swap ? id[i - 1] : id[i];
+      key[i - 1] = hi, key[i] = lo;
+      id[i - 1] = hi_id, id[i] = lo_id;
     }
-    if (j == 0) most = val;
+  uint64_t ids_left = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) ids_left |= uint64_t(id[i]) << (4 * i);
+  if (PER <= 8) ids_left = uint32_t(ids_left);
+
+  // Lane j keeps slot j: the largest first key, of the first lane that has it.
+  int mine = -1;
+  uint32_t mine_key = 0;
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t m = wave_max(key[0]);
+    if (m <= kNoKey) break;
+    const int l = __ffsll((unsigned long long)__ballot(key[0] == m)) - 1;
+    const int e = l * PER + (PER > 1 ? __builtin_amdgcn_readlane(int(ids_left), l) & 15 : 0);
     if (lane == j) {
       mine = e;
-      picked = expf(val - most);
+      mine_key = m;
+    }
+    if (lane == l) {
+#pragma unroll
+      for (int i = 0; i + 1 < PER; ++i) key[i] = key[i + 1];
+      key[PER - 1] = 0;
+      if (PER <= 8) ids_left = uint32_t(ids_left) >> 4;
+      else ids_left >>= 4;
     }
   }
-  float total;
-  if (p.renorm) {
-    total = picked;
-  } else {
+  const float most = of_key(uint32_t(__builtin_amdgcn_readlane(int(mine_key), 0)));
+  const float picked = mine >= 0 ? exp_of(of_key(mine_key) - most) : 0.0f;
+  float total = picked;
+  if (!p.renorm) {
     total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) total += v[i] == -__builtin_inff() ? 0.0f : expf(v[i] - most);
+    for (int i = 0; i < PER; ++i) total += v[i] == -__builtin_inff() ? 0.0f : exp_of(v[i] - most);
   }
   total = wave_sum(total);
   if (lane < p.k) {
@@ -179,7 +300,7 @@ __device__ inline int first_rows(int32_t* counts, int E) {
       const int c = e < E ? counts[e] : 0;
       const int in = wave_scan(c);
       if (e < E) counts[e] = at + in - c;
-      at += __shfl(in, 63);
+      at += __builtin_amdgcn_readlane(in, 63);
     }
     if (threadIdx.x == 0) all = at;
   }
@@ -193,7 +314,12 @@ __global__ __launch_bounds__(kThreads) void route_small(const RouteParams p) {
   __shared__ uint16_t hist[kWaves][kMaxE];
   __shared__ int32_t run[kMaxE];
   const int tid = threadIdx.x, wave = tid >> 6;
-  for (int t = wave; t < p.tokens; t += kWaves) choose<PER>(p, t, ids + t * p.k);
+  const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
+  for (int t = wave; t < p.tokens; t += kWaves) {
+    Row<PER> row;
+    row.load(p.logits, t * p.stride, p.E, p.dtype, vec);
+    choose<PER>(p, t, row.v, ids + t * p.k);
+  }
   for (int i = tid; i < p.E; i += kThreads) run[i] = 0;
   __syncthreads();
   const int n = p.tokens * p.k;
@@ -224,10 +350,18 @@ __global__ __launch_bounds__(kThreads) void route_choose(const RouteParams p, in
   __shared__ uint16_t hist[kWaves][kMaxE];
   __shared__ int32_t run[kMaxE];
   const int tid = threadIdx.x, wave = tid >> 6;
+  const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
   for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int t0 = b * kRouteTokens;
     const int nt = p.tokens - t0 < kRouteTokens ? p.tokens - t0 : kRouteTokens;
-    for (int t = wave; t < nt; t += kWaves) choose<PER>(p, t0 + t, ids + t * p.k);
+    // The next token's logits are on their way while one is chosen from.
+    Row<PER> row, next;
+    if (wave < nt) next.load(p.logits, (t0 + wave) * p.stride, p.E, p.dtype, vec);
+    for (int t = wave; t < nt; t += kWaves) {
+      row = next;
+      if (t + kWaves < nt) next.load(p.logits, (t0 + t + kWaves) * p.stride, p.E, p.dtype, vec);
+      choose<PER>(p, t0 + t, row.v, ids + t * p.k);
+    }
     for (int i = tid; i < p.E; i += kThreads) run[i] = 0;
     __syncthreads();
     const int n = nt * p.k;
@@ -250,7 +384,7 @@ __global__ __launch_bounds__(64) void route_scan(const RouteParams p, int blocks
     const int c = b + lane < blocks ? h[b + lane] : 0;
     const int in = wave_scan(c);
     if (b + lane < blocks) h[b + lane] = at + in - c;
-    at += __shfl(in, 63);
+    at += __builtin_amdgcn_readlane(in, 63);
   }
   if (lane == 0) p.counts[e] = at;
 }
@@ -281,62 +415,69 @@ __global__ __launch_bounds__(kThreads) void route_place(const RouteParams p, int
 template <int PER>
 __global__ __launch_bounds__(256) void route_back(const RouteBackParams p) {
   const int lane = threadIdx.x & 63;
-  for (int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); t < p.tokens;
-       t += int64_t(gridDim.x) * 4) {
-    int e = -1;
-    float w = 0.0f, dw = 0.0f;
-    if (lane < p.k) {
-      const int64_t s = t * p.k + lane;
-      e = p.experts[s];
-      if (e >= p.E) e = -1;
-      if (e >= 0) {
-        w = p.weights[s];
-        dw = p.dweights[s];
-      }
+  const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
+  const bool vec_out = row_pieces<PER>(p.dlogits, p.E, p.E, p.dtype);
+  const int64_t step = int64_t(gridDim.x) * 4;
+  struct Slots {
+    int e;
+    float w, dw;
+  };
+  auto slots = [&](int64_t t) {
+    Slots s{-1, 0.0f, 0.0f};
+    if (lane < p.k) s = Slots{p.experts[t * p.k + lane], p.weights[t * p.k + lane],
+                              p.dweights[t * p.k + lane]};
+    return s;
+  };
+  int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  Row<PER> next;
+  Slots next_slots{-1, 0.0f, 0.0f};
+  if (t < p.tokens) {
+    next_slots = slots(t);
+    if (!p.renorm) next.load(p.logits, t * p.stride, p.E, p.dtype, vec);
+  }
+  for (; t < p.tokens; t += step) {
+    const Row<PER> row = next;
+    Slots s = next_slots;
+    if (t + step < p.tokens) {  // on their way while this token is done
+      next_slots = slots(t + step);
+      if (!p.renorm) next.load(p.logits, (t + step) * p.stride, p.E, p.dtype, vec);
     }
-    const float mean = wave_sum(e >= 0 ? w * dw : 0.0f);
+    if (s.e >= p.E) s.e = -1;
+    const float mean = wave_sum(s.e >= 0 ? s.w * s.dw : 0.0f);
     float q[PER], gr[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) q[i] = gr[i] = 0.0f;
     if (!p.renorm) {
-      float most = -__builtin_inff();
+      float most = row.v[0];  // of the numbers: a NaN makes the sum NaN by itself
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int x = i * 64 + lane;
-        q[i] = x < p.E ? load_value(p.logits, t * p.stride + x, p.dtype) : -__builtin_inff();
-        most = q[i] > most || q[i] != q[i] ? q[i] : most;
-      }
-#pragma unroll
-      for (int d = 32; d; d >>= 1) {
-        const float u = __shfl_xor(most, d);
-        most = u > most || u != u ? u : most;
-      }
-      if (most == -__builtin_inff()) most = 0.0f;
+      for (int i = 1; i < PER; ++i) most = fmaxf(most, row.v[i]);
+      most = wave_fmax(most);
       float total = 0.0f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        q[i] = q[i] == -__builtin_inff() ? 0.0f : expf(q[i] - most);
+        q[i] = row.v[i] == -__builtin_inff() ? 0.0f : exp_of(row.v[i] - most);
         total += q[i];
       }
       total = wave_sum(total);
+      const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) q[i] = total == 0.0f ? 0.0f : q[i] / total;
+      for (int i = 0; i < PER; ++i) q[i] *= inverse;
     }
     for (int j = 0; j < p.k; ++j) {
-      const int ej = __shfl(e, j);
-      const float wj = __shfl(w, j), dj = __shfl(dw, j);
+      const int ej = __builtin_amdgcn_readlane(s.e, j);
+      const float wj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s.w), j));
+      const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s.dw), j));
+      const bool here = ej >= 0 && lane == ej / PER;
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (ej == i * 64 + lane) {
-          gr[i] = dj;
-          if (p.renorm) q[i] = wj;
+        if (ej % PER == i) {  // the same for the whole wave
+          gr[i] = here ? dj : gr[i];
+          if (p.renorm) q[i] = here ? wj : q[i];
         }
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int x = i * 64 + lane;
-      if (x < p.E) store_value(p.dlogits, t * p.E + x, p.dtype, q[i] == 0.0f ? 0.0f : q[i] * (gr[i] - mean));
-    }
+    for (int i = 0; i < PER; ++i) gr[i] = q[i] == 0.0f ? 0.0f : q[i] * (gr[i] - mean);
+    Row<PER>::store(p.dlogits, t * p.E, p.E, p.dtype, vec_out, gr);
   }
 }
 
@@ -378,7 +519,7 @@ hipError_t launch_route_back(const RouteBackParams& p, hipStream_t stream) {
   if (p.tokens == 0) return hipSuccess;
   (void)hipGetLastError();
   const int64_t want = (int64_t(p.tokens) + 3) / 4;
-  const int grid = int(want < 65536 ? want : 65536);
+  const int grid = int(want < 2048 ? want : 2048);  // 8 waves per SIMD
   with_per(p.E, [&](auto per) {
     route_back<decltype(per)::value><<<dim3(grid), dim3(256), 0, stream>>>(p);
   });
