@@ -34,64 +34,82 @@ struct Elem<A2AV_FP32> {
   __device__ static float down(float v) { return v; }
 };
 
-// N elements at p, as floats; N * size is 16 when the rows are aligned, else
-// N is 1.
-template <int DT, int N>
-__device__ inline void load_n(const typename Elem<DT>::type* p, float (&v)[N]) {
-  using T = typename Elem<DT>::type;
-  struct alignas(sizeof(T) * N) Pack {
-    T e[N];
-  };
-  const Pack k = *reinterpret_cast<const Pack*>(p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = Elem<DT>::up(k.e[i]);
+// N elements as they lie in memory, 16 bytes of them where a row has as many.
+// ALIGNED: at a multiple of their size; else at any element (the loads and
+// stores are the same instructions, which take every address).  Kept apart from
+// their values as floats, so that several are in flight before the first is
+// looked at.
+template <int DT, int N, bool ALIGNED>
+struct __attribute__((packed, aligned(ALIGNED ? sizeof(typename Elem<DT>::type) * N
+                                              : sizeof(typename Elem<DT>::type)))) Pack {
+  typename Elem<DT>::type e[N];
+  __device__ float operator[](int i) const { return Elem<DT>::up(e[i]); }
+};
+
+template <int DT, int N, bool ALIGNED>
+__device__ inline Pack<DT, N, ALIGNED> load_n(const typename Elem<DT>::type* p) {
+  return *reinterpret_cast<const Pack<DT, N, ALIGNED>*>(p);
 }
 
-template <int DT, int N>
+// STREAM: past the caches.  Of 235 MB of dequantised rows it made 67 us into 48,
+// of combined rows (117 MB) 261 into 241; where half of the bytes are stores to
+// scattered rows (the combine's gradient) it changed nothing.
+template <int DT, int N, bool ALIGNED, bool STREAM = false>
 __device__ inline void store_n(typename Elem<DT>::type* p, const float (&v)[N]) {
-  using T = typename Elem<DT>::type;
-  struct alignas(sizeof(T) * N) Pack {
-    T e[N];
-  } k;
+  Pack<DT, N, ALIGNED> k;
 #pragma unroll
   for (int i = 0; i < N; ++i) k.e[i] = Elem<DT>::down(v[i]);
-  *reinterpret_cast<Pack*>(p) = k;
+  if constexpr (STREAM && ALIGNED && sizeof(k) == 16)
+    __builtin_nontemporal_store(__builtin_bit_cast(uint4v, k), reinterpret_cast<uint4v*>(p));
+  else
+    *reinterpret_cast<Pack<DT, N, ALIGNED>*>(p) = k;
+}
+
+// Where piece i of a row begins: the last one is moved back to end with the row
+// (its first elements are the one before's last).
+template <int N>
+__device__ inline int piece_at(int i, int width) {
+  return i * N + N <= width ? i * N : width - N;
 }
 
 constexpr int kSlots = 8;  // slots whose rows are in flight together
 
 // A token's row in pieces of N elements, one piece per lane; `across` lanes
-// (a power of two, 256 at most) per token and workgroup column.
-template <int DT, int N>
+// (a power of two, 256 at most) per token and workgroup column.  WAVE: across
+// is 64 at least, so that a wave has one token and its places and weights are
+// scalars.  The rows of eight slots are loaded before the first is used; an
+// empty slot loads nothing then, else row 0, whose value it drops.
+template <int DT, int N, bool ALIGNED, bool WAVE>
 __global__ __launch_bounds__(256) void combine_kernel(const CombineParams p, int across) {
   using T = typename Elem<DT>::type;
-  const int pieces = p.width / N;
+  const int pieces = (p.width + N - 1) / N;
   const int per_wg = 256 / across;
   const int piece0 = blockIdx.y * across + (threadIdx.x & (across - 1));
-  for (int64_t t = int64_t(blockIdx.x) * per_wg + threadIdx.x / across; t < p.tokens;
-       t += int64_t(gridDim.x) * per_wg) {
+  for (int64_t t0 = int64_t(blockIdx.x) * per_wg; t0 < p.tokens; t0 += int64_t(gridDim.x) * per_wg) {
+    int64_t t = t0 + threadIdx.x / across;
+    if (WAVE) t = t0 + __builtin_amdgcn_readfirstlane(threadIdx.x / across);
+    if (t >= p.tokens) continue;
     const int32_t* place = p.place + t * p.k;
     const float* w = p.weights ? p.weights + t * p.k : nullptr;
     for (int piece = piece0; piece < pieces; piece += gridDim.y * across) {
+      const int at = piece_at<N>(piece, p.width);
       float sum[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) sum[i] = 0.0f;
       for (int j0 = 0; j0 < p.k; j0 += kSlots) {
-        float v[kSlots][N];
+        Pack<DT, N, ALIGNED> v[kSlots];
         float wj[kSlots];
         bool here[kSlots];
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
-          here[j] = false;
-          if (j0 + j < p.k) {
-            const int64_t r = place[j0 + j];
-            here[j] = r >= 0 && r < p.y_rows;
-            if (!here[j] && r != -1 && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
-            if (here[j]) {
-              wj[j] = w ? w[j0 + j] : 1.0f;
-              load_n<DT, N>(static_cast<const T*>(p.y) + r * p.y_stride + int64_t(piece) * N, v[j]);
-            }
-          }
+          const bool slot = j0 + j < p.k;
+          const int32_t r = slot ? place[j0 + j] : -1;
+          here[j] = r >= 0 && r < p.y_rows;
+          if (!here[j] && r != -1 && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
+          wj[j] = here[j] ? (w ? w[j0 + j] : 1.0f) : 0.0f;
+          if (WAVE ? here[j] : slot && p.y_rows > 0)
+            v[j] = load_n<DT, N, ALIGNED>(static_cast<const T*>(p.y) +
+                                          int64_t(here[j] ? r : 0) * p.y_stride + at);
         }
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
@@ -100,22 +118,22 @@ __global__ __launch_bounds__(256) void combine_kernel(const CombineParams p, int
             for (int i = 0; i < N; ++i) sum[i] = fmaf(wj[j], v[j][i], sum[i]);
           }
       }
-      store_n<DT, N>(static_cast<T*>(p.out) + t * p.o_stride + int64_t(piece) * N, sum);
+      store_n<DT, N, ALIGNED, true>(static_cast<T*>(p.out) + t * p.o_stride + at, sum);
     }
   }
 }
 
-// One workgroup per token: dout's row is read once for all slots, each slot's
+// One workgroup per token: dout's row is read once for eight slots, each slot's
 // row of y once, and its row of dy is written in the same pass.
-template <int DT, int N, int THREADS>
+template <int DT, int N, bool ALIGNED, int THREADS>
 __global__ __launch_bounds__(THREADS) void combine_back_kernel(const CombineParams p) {
   using T = typename Elem<DT>::type;
   __shared__ float part[THREADS / 64][kSlots];
-  const int pieces = p.width / N;
+  const int pieces = (p.width + N - 1) / N;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
     for (int j0 = 0; j0 < p.k; j0 += kSlots) {
-      int64_t row[kSlots];
+      int32_t row[kSlots];
       float w[kSlots], dot[kSlots];
 #pragma unroll
       for (int j = 0; j < kSlots; ++j) {
@@ -123,7 +141,7 @@ __global__ __launch_bounds__(THREADS) void combine_back_kernel(const CombinePara
         w[j] = 1.0f;
         dot[j] = 0.0f;
         if (j0 + j < p.k) {
-          const int64_t r = p.place[t * p.k + j0 + j];
+          const int32_t r = p.place[t * p.k + j0 + j];
           if (r >= 0 && r < p.y_rows)
             row[j] = r;
           else if (r != -1 && p.status && tid == 0)
@@ -131,29 +149,37 @@ __global__ __launch_bounds__(THREADS) void combine_back_kernel(const CombinePara
           if (p.weights) w[j] = p.weights[t * p.k + j0 + j];
         }
       }
+      const bool want_dots = p.dweights != nullptr;
       for (int piece = tid; piece < pieces; piece += THREADS) {
-        float d[N], v[kSlots][N];
-        load_n<DT, N>(static_cast<const T*>(p.dout) + t * p.o_stride + int64_t(piece) * N, d);
-        if (p.dweights) {
+        const int at = piece_at<N>(piece, p.width);
+        const auto d = load_n<DT, N, ALIGNED>(static_cast<const T*>(p.dout) + t * p.o_stride + at);
+        Pack<DT, N, ALIGNED> v[kSlots];
+        if (want_dots) {
 #pragma unroll
           for (int j = 0; j < kSlots; ++j)
             if (row[j] >= 0)
-              load_n<DT, N>(static_cast<const T*>(p.y) + row[j] * p.y_stride + int64_t(piece) * N,
-                            v[j]);
+              v[j] = load_n<DT, N, ALIGNED>(static_cast<const T*>(p.y) +
+                                            int64_t(row[j]) * p.y_stride + at);
         }
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
           if (row[j] >= 0) {
             float g[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              g[i] = w[j] * d[i];
-              if (p.dweights) dot[j] = fmaf(d[i], v[j][i], dot[j]);
-            }
-            store_n<DT, N>(static_cast<T*>(p.dy) + row[j] * p.dy_stride + int64_t(piece) * N, g);
+            for (int i = 0; i < N; ++i) g[i] = w[j] * d[i];
+            store_n<DT, N, ALIGNED>(static_cast<T*>(p.dy) + int64_t(row[j]) * p.dy_stride + at, g);
           }
+        if (want_dots) {
+#pragma unroll
+          for (int j = 0; j < kSlots; ++j)
+            if (row[j] >= 0) {
+#pragma unroll
+              for (int i = 0; i < N; ++i)
+                if (ALIGNED || at + i >= piece * N) dot[j] = fmaf(d[i], v[j][i], dot[j]);
+            }
+        }
       }
-      if (p.dweights) {
+      if (want_dots) {
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
 #pragma unroll
@@ -190,14 +216,18 @@ __global__ __launch_bounds__(256) void quantize_kernel(const Mx4Params p) {
     float v[8];
     if constexpr (WHOLE) {
       if constexpr (DT == A2AV_FP32) {
-        float lo[4], hi[4];
-        load_n<DT, 4>(x, lo);
-        load_n<DT, 4>(x + 4, hi);
+        const auto lo = load_n<DT, 4, true>(x), hi = load_n<DT, 4, true>(x + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = lo[i], v[i + 4] = hi[i];
       } else {
-        load_n<DT, 8>(x, v);
+        const auto w = load_n<DT, 8, true>(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = w[i];
       }
+    } else if (col + 8 <= p.cols) {
+      const auto w = load_n<DT, 8, false>(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = w[i];
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = col + i < p.cols ? Elem<DT>::up(x[i]) : 0.0f;
@@ -257,11 +287,13 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4Params p) {
     if constexpr (WHOLE) {
       if constexpr (DT == A2AV_FP32) {
         const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-        store_n<DT, 4>(x, lo);
-        store_n<DT, 4>(x + 4, hi);
+        store_n<DT, 4, true, true>(x, lo);
+        store_n<DT, 4, true, true>(x + 4, hi);
       } else {
-        store_n<DT, 8>(x, v);
+        store_n<DT, 8, true, true>(x, v);
       }
+    } else if (col + 8 <= p.cols) {
+      store_n<DT, 8, false>(x, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -293,45 +325,55 @@ bool aligned(int dtype, int64_t width, const void* a, int64_t sa, const void* b,
 
 }  // namespace
 
+// f(pieces' length, whether they are aligned) for rows of `width` elements.
+template <int DT, class F>
+static void with_pieces(bool fast, int width, F f) {
+  constexpr int N = DT == A2AV_FP32 ? 4 : 8;
+  using One = std::integral_constant<int, 1>;
+  using Many = std::integral_constant<int, N>;
+  if (fast) f(Many{}, std::true_type{});
+  else if (width >= N) f(Many{}, std::false_type{});
+  else f(One{}, std::false_type{});
+}
+
 hipError_t launch_combine(const CombineParams& p, hipStream_t stream) {
   const bool fast = aligned(p.dtype, p.width, p.y, p.y_stride, p.out, p.o_stride, nullptr, 0);
-  const int n = fast ? 16 / size_of(p.dtype) : 1;
-  const int pieces = p.width / n;
-  int across = 1;
-  while (across < pieces && across < 256) across *= 2;
-  const int64_t wgs = (int64_t(p.tokens) * across + 255) / 256;
-  const int cols = (pieces + across - 1) / across;
-  const dim3 grid(uint32_t(wgs < (1 << 20) ? wgs : (1 << 20)), uint32_t(cols < 64 ? cols : 64));
   return with_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    constexpr int N = DT == A2AV_FP32 ? 4 : 8;
-    if (fast)
-      combine_kernel<DT, N><<<grid, dim3(256), 0, stream>>>(p, across);
-    else
-      combine_kernel<DT, 1><<<grid, dim3(256), 0, stream>>>(p, across);
+    with_pieces<DT>(fast, p.width, [&](auto n, auto is_aligned) {
+      constexpr int N = decltype(n)::value;
+      constexpr bool kAligned = decltype(is_aligned)::value;
+      const int pieces = (p.width + N - 1) / N;
+      // The power of two that leaves the fewest lanes without a piece.
+      int across = 1;
+      while (across < pieces && across < 256) across *= 2;
+      const auto lanes = [&](int a) { return (pieces + a - 1) / a * a; };
+      while (across > 64 && lanes(across / 2) < lanes(across)) across /= 2;
+      const int64_t wgs = (int64_t(p.tokens) * across + 255) / 256;
+      const int cols = (pieces + across - 1) / across;
+      const dim3 grid(uint32_t(wgs < (1 << 20) ? wgs : (1 << 20)), uint32_t(cols < 64 ? cols : 64));
+      if (across >= 64)
+        combine_kernel<DT, N, kAligned, true><<<grid, dim3(256), 0, stream>>>(p, across);
+      else
+        combine_kernel<DT, N, kAligned, false><<<grid, dim3(256), 0, stream>>>(p, across);
+    });
   });
 }
 
 hipError_t launch_combine_back(const CombineParams& p, hipStream_t stream) {
   const bool fast = aligned(p.dtype, p.width, p.y, p.y_stride, p.dout, p.o_stride, p.dy,
                             p.dy_stride);
-  const int n = fast ? 16 / size_of(p.dtype) : 1;
-  const int pieces = p.width / n;
   const dim3 grid(uint32_t(p.tokens < (1 << 20) ? p.tokens : (1 << 20)));
   return with_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    constexpr int N = DT == A2AV_FP32 ? 4 : 8;
-    if (pieces <= 64) {
-      if (fast)
-        combine_back_kernel<DT, N, 64><<<grid, dim3(64), 0, stream>>>(p);
+    with_pieces<DT>(fast, p.width, [&](auto n, auto is_aligned) {
+      constexpr int N = decltype(n)::value;
+      constexpr bool kAligned = decltype(is_aligned)::value;
+      if ((p.width + N - 1) / N <= 64)
+        combine_back_kernel<DT, N, kAligned, 64><<<grid, dim3(64), 0, stream>>>(p);
       else
-        combine_back_kernel<DT, 1, 64><<<grid, dim3(64), 0, stream>>>(p);
-    } else {
-      if (fast)
-        combine_back_kernel<DT, N, 256><<<grid, dim3(256), 0, stream>>>(p);
-      else
-        combine_back_kernel<DT, 1, 256><<<grid, dim3(256), 0, stream>>>(p);
-    }
+        combine_back_kernel<DT, N, kAligned, 256><<<grid, dim3(256), 0, stream>>>(p);
+    });
   });
 }
 
