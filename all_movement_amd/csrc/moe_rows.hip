@@ -46,14 +46,19 @@ struct __attribute__((packed, aligned(ALIGNED ? sizeof(typename Elem<DT>::type) 
   __device__ float operator[](int i) const { return Elem<DT>::up(e[i]); }
 };
 
-template <int DT, int N, bool ALIGNED>
+// STREAM, here and below: past the caches.  Stores: 235 MB of dequantised rows
+// took 67 us and take 48.  Loads: to combine 65536 rows of 14 KiB took 255 us and
+// takes 208.  Where half of the bytes are stores to scattered rows (the combine's
+// gradient) it changed nothing.
+template <int DT, int N, bool ALIGNED, bool STREAM = false>
 __device__ inline Pack<DT, N, ALIGNED> load_n(const typename Elem<DT>::type* p) {
-  return *reinterpret_cast<const Pack<DT, N, ALIGNED>*>(p);
+  using P = Pack<DT, N, ALIGNED>;
+  if constexpr (STREAM && ALIGNED && sizeof(P) == 16)
+    return __builtin_bit_cast(P, __builtin_nontemporal_load(reinterpret_cast<const uint4v*>(p)));
+  else
+    return *reinterpret_cast<const P*>(p);
 }
 
-// STREAM: past the caches.  Of 235 MB of dequantised rows it made 67 us into 48,
-// of combined rows (117 MB) 261 into 241; where half of the bytes are stores to
-// scattered rows (the combine's gradient) it changed nothing.
 template <int DT, int N, bool ALIGNED, bool STREAM = false>
 __device__ inline void store_n(typename Elem<DT>::type* p, const float (&v)[N]) {
   Pack<DT, N, ALIGNED> k;
@@ -108,8 +113,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const CombineParams p, int
           if (!here[j] && r != -1 && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
           wj[j] = here[j] ? (w ? w[j0 + j] : 1.0f) : 0.0f;
           if (WAVE ? here[j] : slot && p.y_rows > 0)
-            v[j] = load_n<DT, N, ALIGNED>(static_cast<const T*>(p.y) +
-                                          int64_t(here[j] ? r : 0) * p.y_stride + at);
+            v[j] = load_n<DT, N, ALIGNED, true>(static_cast<const T*>(p.y) +
+                                                int64_t(here[j] ? r : 0) * p.y_stride + at);
         }
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
