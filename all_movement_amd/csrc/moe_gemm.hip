@@ -268,38 +268,43 @@ __device__ inline int4v load_part(const uint8_t* p, int n) {
 // pieces of 8 or 16 bytes become rows, which leave in whole lines.  Straight
 // from the fragments every line of the output was written in four parts, and a
 // 256 x 256 tile took 14 us to store.
-template <int MODE, int TM, int TN, int FM, int FN, int ES>
+// Half the sums at a time if all of them do not fit into kBytes.
+template <int MODE, int TM, int TN, int FM, int FN, int ES, int kBytes>
 __device__ inline void store_rows(const GmmParams& p, const Tile& t, const float4v (&acc)[FM][FN],
-                                  int wm, int wn, uint8_t* lds, int bytes) {
+                                  int wm, int wn, uint8_t* lds) {
   constexpr int kRow = TN * ES, kChunks = kRow / 16;
   constexpr int kSwizzle = (kChunks < 16 ? kChunks : 16) - 1;
+  constexpr int kBatch = kRow * TM <= kBytes ? FM : FM / 2;  // fragment rows at once
+  static_assert(kBatch * 16 * kRow <= kBytes, "the batch fits");
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
-  const int batch = bytes / (kRow * 16) < FM ? bytes / (kRow * 16) : FM;  // fragment rows at once
   const int64_t first = MODE == kGmmDw ? int64_t(t.span.e) * p.N + t.out_row0 : t.out_row0;
   const int64_t col0 = t.c0 + wn * TN;
   const int cols = t.cn - wn * TN;
   const bool wide = ((p.out_stride * ES) & 15) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
 #pragma unroll
-  for (int a = 0; a < FM; ++a) {
-    const int at = a % batch;
-    uint8_t* row = lds + (at * 16 + l16) * kRow;
+  for (int a0 = 0; a0 < FM; a0 += kBatch) {
 #pragma unroll
-    for (int d = 0; d < FN; ++d) {
-      if constexpr (ES == 4) {
-        *reinterpret_cast<float4v*>(row + ((d * 4 + g) ^ (l16 & kSwizzle)) * 16) = acc[a][d];
-      } else {
-        uint16_t h[4];
+    for (int a = 0; a < kBatch; ++a) {
+      uint8_t* row = lds + (a * 16 + l16) * kRow;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = round16(acc[a][d][i], p.out_type);
-        *reinterpret_cast<uint64_t*>(row + ((d * 2 + (g >> 1)) ^ (l16 & kSwizzle)) * 16 +
-                                     (g & 1) * 8) = __builtin_bit_cast(uint64_t, h);
+      for (int d = 0; d < FN; ++d) {
+        const float4v v = acc[a0 + a][d];
+        if constexpr (ES == 4) {
+          *reinterpret_cast<float4v*>(row + ((d * 4 + g) ^ (l16 & kSwizzle)) * 16) = v;
+        } else {
+          uint16_t h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = round16(v[i], p.out_type);
+          *reinterpret_cast<uint64_t*>(row + ((d * 2 + (g >> 1)) ^ (l16 & kSwizzle)) * 16 +
+                                       (g & 1) * 8) = __builtin_bit_cast(uint64_t, h);
+        }
       }
     }
-    if (at + 1 < batch && a + 1 < FM) continue;
     constexpr int kAtOnce = 64 / kChunks;  // rows per store of the wave
-    for (int r = lane / kChunks; r < (at + 1) * 16; r += kAtOnce) {
-      const int out_row = wm * TM + (a - at) * 16 + r;
-      const int ch = lane % kChunks, col = ch * (16 / ES);
+    const int ch = lane % kChunks, col = ch * (16 / ES);
+#pragma unroll 4
+    for (int r = lane / kChunks; r < kBatch * 16; r += kAtOnce) {
+      const int out_row = wm * TM + a0 * 16 + r;
       const int4v v = *reinterpret_cast<const int4v*>(lds + r * kRow + (ch ^ (r & kSwizzle)) * 16);
       if (out_row >= t.rm || col >= cols) continue;
       uint8_t* o = p.out + ((first + out_row) * p.out_stride + col0 + col) * ES;
@@ -317,7 +322,10 @@ __device__ inline void store_rows(const GmmParams& p, const Tile& t, const float
 
 // Chunk c of row r of an across tile lies at c ^ across_swizzle(r), so that the
 // transposing read, 4 rows x 32 bytes by 16 lanes, meets every bank once.
-__device__ inline int across_swizzle(int r) { return 2 * (r & 3) | (8 & r); }
+template <int SPAN>
+__device__ inline int across_swizzle(int r) {
+  return (2 * (r & 3) | (8 & r)) & (SPAN / 8 - 1);
+}
 
 // One operand's tile of SPAN outputs x 128 bytes of reduction, loaded by NW
 // waves as 16-byte chunks.
@@ -332,7 +340,7 @@ struct Loader {
   static_assert(kChunks % (NW * 64) == 0, "a tile is a whole number of wave loads");
   const uint8_t* ptr[kPer];
   int32_t left[kPer];   // along: elements of the row from this chunk on; across: columns from it
-  int4v staged[DIRECT ? 1 : kPer];
+  int4v staged[2][DIRECT ? 1 : kPer];  // steps of even and odd number
   int wave, lane;
 
   __device__ int chunk(int i) const { return (wave * kPer + i) * 64 + lane; }
@@ -340,9 +348,20 @@ struct Loader {
   __device__ int lds_row(int i) const { return ALONG ? chunk(i) / 8 : chunk(i) / (SPAN / 8); }
   __device__ int col(int i) const {
     const int r = lds_row(i);
-    return ALONG ? (chunk(i) % 8) ^ (r & 7) : (chunk(i) % (SPAN / 8)) ^ across_swizzle(r);
+    return ALONG ? (chunk(i) % 8) ^ (r & 7) : (chunk(i) % (SPAN / 8)) ^ across_swizzle<SPAN>(r);
   }
 };
+
+// A sum may be looked at 7 wait states after its last product at the earliest.
+// The compiler keeps that distance along a straight run of code, but not across
+// the branch at a loop's end (nor for products written in asm): every run of
+// products ends with it.  Without it a 64 x 64 tile of one step lost the last
+// register of its last sums.
+__device__ inline void end_of_products() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 7");
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 template <int TY>
 __device__ inline float4v mma(int4v a, int4v b, float4v c) {
@@ -434,7 +453,8 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
   const uint32_t lds0 = uint32_t(uintptr_t((lds_u8*)lds));
 
   // Loads step k into buffer k & 1 (or, not DIRECT, into registers).
-  auto load_one = [&](auto& ld, auto along, int i, int k, uint32_t base, const uint8_t* ptr) {
+  auto load_one = [&](auto& ld, auto along, int i, int k, auto odd, uint32_t base,
+                      const uint8_t* ptr) {
     constexpr bool kAlong = decltype(along)::value;
     int n;  // elements of the chunk that exist
     if (kAlong) {
@@ -447,7 +467,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       load_to_lds(n > 0 ? ptr : zeros,
                   __builtin_amdgcn_readfirstlane(base + (wave * ld.kPer + i) * 1024));
     } else {
-      ld.staged[i] = n > 0 ? load_part(ptr, n) : int4v{0, 0, 0, 0};
+      ld.staged[decltype(odd)::value][i] = n > 0 ? load_part(ptr, n) : int4v{0, 0, 0, 0};
     }
   };
   // dw: the rows of x of the next step to issue, read a step ahead so that
@@ -479,7 +499,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       }
     }
   };
-  auto issue = [&](int k) {
+  auto issue = [&](int k, auto odd) {
     check_rows(k);
     const uint32_t base = lds0 + (k & 1) * kBuf;
     constexpr auto row_kind = std::integral_constant<bool, kRowsAlong>{};
@@ -488,7 +508,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
     for (int i = 0; i < q.kPer; ++i) {
       const uint8_t* ptr = q.ptr[i];
       if (ptr) ptr += kRowsAlong ? int64_t(k) * 128 : int64_t(k) * 64 * p.row_stride;
-      load_one(q, row_kind, i, k, base, ptr);
+      load_one(q, row_kind, i, k, odd, base, ptr);
     }
 #pragma unroll
     for (int i = 0; i < c.kPer; ++i) {
@@ -501,18 +521,19 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
         const int row = next_row[i];
         ptr = row < 0 ? nullptr : ptr + int64_t(row) * p.other_stride;
       }
-      load_one(c, col_kind, i, k, base + BM * 128, ptr);
+      load_one(c, col_kind, i, k, odd, base + BM * 128, ptr);
     }
   };
-  auto put_staged = [&](int k) {
+  auto put_staged = [&](auto odd) {
     if constexpr (!DIRECT) {
-      uint8_t* b = lds + (k & 1) * kBuf;
+      constexpr int kOdd = decltype(odd)::value;
+      uint8_t* b = lds + kOdd * kBuf;
 #pragma unroll
       for (int i = 0; i < q.kPer; ++i)
-        *reinterpret_cast<int4v*>(b + q.chunk(i) * 16) = q.staged[i];
+        *reinterpret_cast<int4v*>(b + q.chunk(i) * 16) = q.staged[kOdd][i];
 #pragma unroll
       for (int i = 0; i < c.kPer; ++i)
-        *reinterpret_cast<int4v*>(b + BM * 128 + c.chunk(i) * 16) = c.staged[i];
+        *reinterpret_cast<int4v*>(b + BM * 128 + c.chunk(i) * 16) = c.staged[kOdd][i];
     }
   };
 
@@ -551,7 +572,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       return *reinterpret_cast<const int4v*>(tile_lds + r * 128 + ch * 16);
     } else {
       const int r = kk * 32 + g * 8 + (l16 >> 2);
-      const int ch = (first / 8 + ((l16 & 3) >> 1)) ^ (2 * (l16 >> 2) | (8 * (g & 1)));
+      const int ch = (first / 8 + ((l16 & 3) >> 1)) ^ across_swizzle<kSpan>(r);
       const uint8_t* a = tile_lds + r * (kSpan * 2) + ch * 16 + (l16 & 1) * 8;
       const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
           (__attribute__((address_space(3))) short4v*)(a));
@@ -604,23 +625,46 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
             acc[a][d] = mma<TY>(fc[d], fq[a], acc[a][d]);
         }
     }
+    end_of_products();
   };
 
+  // Loads run kAhead steps ahead: straight to LDS into the other buffer, or by
+  // way of registers, which the step before puts into LDS.
+  constexpr int kAhead = DIRECT ? 1 : 2;
+  constexpr auto kEven = std::integral_constant<int, 0>{};
+  constexpr auto kOdd = std::integral_constant<int, 1>{};
   if (steps > 0) {
     read_rows(0);
-    issue(0);
+    issue(0, kEven);
     read_rows(1);
-    put_staged(0);
+    if (!DIRECT && steps > 1) {
+      issue(1, kOdd);
+      read_rows(2);
+    }
+    put_staged(kEven);
   }
-  for (int k = 0; k < steps; ++k) {
-    wait_loads_and_barrier();
-    if (k + 1 < steps) {
-      issue(k + 1);
-      read_rows(k + 2);
+  auto step = [&](int k, auto odd) {
+    constexpr auto other = std::integral_constant<int, decltype(odd)::value ^ 1>{};
+    if constexpr (DIRECT) {
+      wait_loads_and_barrier();
+    } else {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    }
+    if (k + kAhead < steps) {
+      issue(k + kAhead, odd);
+      read_rows(k + kAhead + 1);
     }
     compute(k);
-    if (k + 1 < steps) put_staged(k + 1);
+    if (k + 1 < steps) put_staged(other);
+  };
+  int k = 0;
+  for (; k + 1 < steps; k += 2) {
+    step(k, kEven);
+    step(k + 1, kOdd);
   }
+  if (k < steps) step(k, kEven);
   if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
 
   store_tile<MODE, TM, TN, FM, FN>(p, t, acc, wm, wn);
@@ -706,23 +750,28 @@ struct Layout {
   }
 };
 
-// acc += a b with the sums in the accumulation registers.
-template <int TY, int BYTE>
+// acc += a b with the sums in the accumulation registers, or with VECTOR in the
+// vector registers.
+#define A2AV_MMA(op, tail, ...)                                                        \
+  if constexpr (VECTOR)                                                                \
+    asm("v_mfma_" op " %0, %1, %2, %0" tail : "+v"(acc) : "v"(a), "v"(b) __VA_ARGS__); \
+  else                                                                                 \
+    asm("v_mfma_" op " %0, %1, %2, %0" tail : "+a"(acc) : "v"(a), "v"(b) __VA_ARGS__)
+template <int TY, int BYTE, bool VECTOR>
 __device__ inline void mma_acc(float4v& acc, int4v a, int4v b, int sa, int sb) {
-  if constexpr (TY == kGmmBF16)
-    asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
-  else if constexpr (TY == kGmmFP16)
-    asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
-  else if constexpr (BYTE == 0)
-    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-        : "+a"(acc)
-        : "v"(a), "v"(b), "v"(sa), "v"(sb));
-  else
-    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] "
-        "op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-        : "+a"(acc)
-        : "v"(a), "v"(b), "v"(sa), "v"(sb));
+  if constexpr (TY == kGmmBF16) {
+    A2AV_MMA("f32_16x16x32_bf16", "");
+  } else if constexpr (TY == kGmmFP16) {
+    A2AV_MMA("f32_16x16x32_f16", "");
+  } else if constexpr (BYTE == 0) {
+    A2AV_MMA("scale_f32_16x16x128_f8f6f4", ", %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4", , "v"(sa),
+             "v"(sb));
+  } else {
+    A2AV_MMA("scale_f32_16x16x128_f8f6f4",
+             ", %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4", , "v"(sa), "v"(sb));
+  }
 }
+#undef A2AV_MMA
 
 // BM x BN of the output by WM x WN waves, one per SIMD, 128 bytes of the
 // reduction (64 elements of 16 bits, 256 of 4) per stage, through two LDS
@@ -843,28 +892,26 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
   static_assert(!kGather || (2 * kSet - NB - 1 >= NB - 1 && NB <= 4), "indexes in time");
   int next_row[kGather ? kC : 1];
   auto index_row = [&](int s, int at) { return s * 64 + wave * kIndexes + at; };
+  typedef __attribute__((address_space(3))) int lds_int;
   auto load_index = [&](int s) {  // the kSet stages from s (a multiple) on
     if constexpr (kGather) {
+      const uint32_t to = extra0 + wave * 1024 + (s / kSet & 3) * 256;
       const int r = index_row(s + lane / kIndexes, lane % kIndexes);
-      const void* src = r < red ? static_cast<const void*>(p.index + t.span.row0 + r)
-                                : static_cast<const void*>(zeros);
-      load_word_to_lds(src, extra0 + wave * 1024 + (s / kSet & 3) * 256);
+      if (p.index)
+        load_word_to_lds(r < red ? static_cast<const void*>(p.index + t.span.row0 + r)
+                                 : static_cast<const void*>(zeros),
+                         to);
+      else
+        *(lds_int*)(uintptr_t(to + lane * 4)) = int(t.span.row0) + r;
     }
   };
   auto read_rows = [&](int s) {  // for the loads of stage s
     if constexpr (kGather) {
-      const int r = C::row(lane);
-      if (p.index) {
-        const uint32_t at = extra0 + wave * 1024 + ((s & (4 * kSet - 1)) * kIndexes + r) * 4;
+      const uint32_t at =
+          extra0 + wave * 1024 + ((s & (4 * kSet - 1)) * kIndexes + C::row(lane)) * 4;
 #pragma unroll
-        for (int i = 0; i < kC; ++i)
-          next_row[i] =
-              ((const __attribute__((address_space(3))) int*)(uintptr_t(at)))[i * C::kRows];
-      } else {
-#pragma unroll
-        for (int i = 0; i < kC; ++i)
-          next_row[i] = int(t.span.row0) + index_row(s, i * C::kRows + r);
-      }
+      for (int i = 0; i < kC; ++i)
+        next_row[i] = ((const lds_int*)(uintptr_t(at)))[i * C::kRows];
     }
   };
   if constexpr (kGather) {
@@ -969,7 +1016,7 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
     }
   };
 
-  if (kGather && p.index) {
+  if (kGather) {
     load_index(0);
     load_index(kSet);
     wait_loads<0>();
@@ -994,6 +1041,9 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
   // first half are spread between them.  One wave load occupies the path to
   // LDS for 16 cycles, as long as a product: 4 waves keep below its rate with
   // one load per 5 products.
+  // Sums from kVector on stay in vector registers: with all 256 accumulation
+  // registers of a lane taken the compiler moves sums about between products.
+  constexpr int kVector = FM * FN < 64 ? FM * FN : kScales ? 60 : 56;
   constexpr int kHalf = FM * FN, kReads = FM + FN, kAll = kQ + kC;
   constexpr int kBarrier = kHalf / 2;
   auto products = [&](int s, auto which, auto fast) {
@@ -1026,8 +1076,12 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
 #pragma unroll
       for (int b = 0; b < FN; ++b) {
         const int n = a * FN + b, m = kk * kHalf + n;
-        mma_acc<TY, kk>(acc[a][b], fc[kk][b], fq[kk][a], sc[kk][kScales ? b : 0],
-                        sq[kk][kScales ? a : 0]);
+        if (a * FN + b >= kVector)
+          mma_acc<TY, kk, true>(acc[a][b], fc[kk][b], fq[kk][a], sc[kk][kScales ? b : 0],
+                                sq[kk][kScales ? a : 0]);
+        else
+          mma_acc<TY, kk, false>(acc[a][b], fc[kk][b], fq[kk][a], sc[kk][kScales ? b : 0],
+                                 sq[kk][kScales ? a : 0]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int r = 0; r < kReads; ++r)
@@ -1044,7 +1098,7 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
             if ((s & 1) == 0) load_scales(s + NB);
           }
           if constexpr (kGather) {
-            if (p.index && (s & (kSet - 1)) == 0) load_index(s + 2 * kSet);
+            if ((s & (kSet - 1)) == 0) load_index(s + 2 * kSet);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -1060,6 +1114,7 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
   auto stage = [&](int s, auto fast) {
     products(s, std::integral_constant<int, 0>{}, fast);
     products(s, std::integral_constant<int, 1>{}, fast);
+    end_of_products();
     read_rows(s + NB + 1);
   };
   int s = 0;
@@ -1072,14 +1127,20 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
 #pragma unroll
   for (int a = 0; a < FM; ++a)
 #pragma unroll
-    for (int b = 0; b < FN; ++b) asm volatile("" : "+a"(acc[a][b]));
+    for (int b = 0; b < FN; ++b) {
+      if (a * FN + b >= kVector)
+        asm volatile("" : "+v"(acc[a][b]));
+      else
+        asm volatile("" : "+a"(acc[a][b]));
+    }
   if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
   __syncthreads();  // everybody's reads and loads are done
   constexpr int kPart = NB * kBuf / NW / 1024 * 1024;
-  if (p.out_type == A2AV_FP32)
-    store_rows<MODE, TM, TN, FM, FN, 4>(p, t, acc, wm, wn, lds + wave * kPart, kPart);
+  constexpr bool kFp32 = MODE == kGmmDw || TY == kGmmMX4;  // the others' types are 16 bits
+  if (kFp32 && p.out_type == A2AV_FP32)
+    store_rows<MODE, TM, TN, FM, FN, 4, kPart>(p, t, acc, wm, wn, lds + wave * kPart);
   else
-    store_rows<MODE, TM, TN, FM, FN, 2>(p, t, acc, wm, wn, lds + wave * kPart, kPart);
+    store_rows<MODE, TM, TN, FM, FN, 2, kPart>(p, t, acc, wm, wn, lds + wave * kPart);
 }
 
 // 256 x 256 tiles, one workgroup per CU.
@@ -1198,6 +1259,7 @@ __global__ __launch_bounds__(512, MT <= 2 ? 4 : 2) void gmm_few(const GmmParams 
           else
             acc[i][f] = mma<TY>(wv[u][f], xv[u][i], acc[i][f]);
         }
+    end_of_products();
   };
   // Waves take groups of U steps in turn.
   const int steps = (K + kStep - 1) / kStep;
@@ -1270,6 +1332,15 @@ hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
     if ((p.nrows / 128 + used / 2) * ((cols + 127) / 128) > 384)
       return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 2>, 256, p, stream);
     return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 4>, 256, p, stream);
+  }
+  if constexpr (TY != kGmmMX4) {
+    const int64_t used = p.E < p.nrows ? p.E : p.nrows;
+    const int64_t cols = ((MODE == kGmmFwd ? p.N : p.K) + 127) / 128;
+    const int64_t rows = MODE == kGmmDw ? int64_t(p.E) * ((p.N + 127) / 128)
+                                        : p.nrows / 128 + used / 2;
+    // Too few tiles for two on every CU: quarters of them.
+    if (rows * cols < 512)
+      return launch_tiles<MODE, 64, 64>(gmm_kernel<TY, MODE, 64, 64, 2, 2, false>, 256, p, stream);
   }
   return launch_tiles<MODE, 128, 128>(gmm_kernel<TY, MODE, 128, 128, 2, 2, TY == kGmmMX4>, 256, p,
                                       stream);

@@ -224,6 +224,16 @@ def test_lengths_around_the_stages(K):
     check_all(gen, [K, 3 * K, 1, 2], 136, 264, torch.bfloat16, tokens=50)
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_every_product_is_in_the_sums_that_are_stored(dt):
+    """One step of the reduction, tiles of every kind: the last products end right
+    before their sums are stored."""
+    gen = torch.Generator().manual_seed(21)
+    for counts, N, K in [([64, 3], 130, 259), ([40, 64], 72, 72), ([300], 264, 64), ([9], 48, 32),
+                         ([64], 264, 264), ([30, 20], 40, 64)]:
+        check_all(gen, counts, N, K, dt)
+
+
 def test_far_rows_take_the_plain_loads():
     """A stride of which 256 rows pass 4 GiB: the same values as close together."""
     gen = torch.Generator().manual_seed(8)
