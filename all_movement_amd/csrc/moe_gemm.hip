@@ -914,17 +914,6 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
         next_row[i] = ((const lds_int*)(uintptr_t(at)))[i * C::kRows];
     }
   };
-  if constexpr (kGather) {
-    if (p.index)  // a look at all of them, so that the loads need none
-      for (int s = 0; s < stages; s += kSet) {
-        const int r = index_row(s + lane / kIndexes, lane % kIndexes);
-        const int x = r < red ? p.index[t.span.row0 + r] : 0;
-        bad_row = bad_row || (r < red && (x < 0 || x >= p.x_rows));
-      }
-  }
-  // A wave that names a row outside x takes the careful loads throughout.
-  const bool careful = __ballot(bad_row) != 0;
-
   // ---- scales: a thread brings 16 bytes of a row of the tile (rows operand
   // first) for two stages.
   constexpr int kS = kScales ? (BM + BN) / (NW * 64) : 1;
@@ -1030,6 +1019,16 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
     for (int i = 0; i < kQ + kC; ++i) load_one(s, i, kCareful);
   }
   read_rows(NB);
+  if constexpr (kGather) {
+    if (p.index)  // a look at all of them, under the first loads, so that the rest need none
+      for (int s = 0; s < stages; s += kSet) {
+        const int r = index_row(s + lane / kIndexes, lane % kIndexes);
+        const int x = r < red ? p.index[t.span.row0 + r] : 0;
+        bad_row = bad_row || (r < red && (x < 0 || x >= p.x_rows));
+      }
+  }
+  // A wave that names a row outside x takes the careful loads throughout.
+  const bool careful = __ballot(bad_row) != 0;
   wait_loads<(NB - 1) * (kQ + kC)>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -1169,14 +1168,14 @@ __global__ __launch_bounds__(256, NB == 2 ? 2 : 1) void gmm_small(const GmmParam
 
 // ------------------------------------------------------------------ few rows per expert
 
-// MT x 16 rows and FN x 16 columns by 8 waves that share out the reduction.
+// MT x 16 rows and FN x 16 columns by NW waves that share out the reduction.
 // With few rows an expert's weight is read for little work, and its bytes are
 // the time: every wave streams its part of W straight into registers (nothing
 // of it is used twice, so LDS would only be a detour), 4 steps of 64 bytes per
 // row at a time, and the waves' sums meet in LDS, in the order of the waves.
-template <int TY, int MT, int FN>
-__global__ __launch_bounds__(512, MT <= 2 ? 4 : 2) void gmm_few(const GmmParams p) {
-  constexpr int NW = 8, BM = MT * 16, BN = FN * 16, U = 4;
+template <int TY, int MT, int FN, int NW>
+__global__ __launch_bounds__(NW * 64, 4) void gmm_few(const GmmParams p) {
+  constexpr int BM = MT * 16, BN = FN * 16, U = 4;
   constexpr int kStep = TY == kGmmMX4 ? 128 : 32;  // reduction elements per product
   __shared__ float part[NW][MT * FN][64 * 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -1192,16 +1191,16 @@ __global__ __launch_bounds__(512, MT <= 2 ? 4 : 2) void gmm_few(const GmmParams 
   const uint8_t* w[FN];
   const uint8_t* xs[TY == kGmmMX4 ? MT : 1];
   const uint8_t* ws[TY == kGmmMX4 ? FN : 1];
-  bool real[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int r = i * 16 + l16;
     int64_t row = t.span.row0 + (r < t.rm ? r : t.rm - 1);
-    if (p.index) row = p.index[row];
-    real[i] = row >= 0 && row < p.x_rows;
-    if (!real[i] && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
-    x[i] = p.rows + (real[i] ? row : 0) * p.row_stride + g * 16;
-    if constexpr (TY == kGmmMX4) xs[i] = p.row_scales + (real[i] ? row : 0) * p.blocks;
+    if (p.index) {  // a row outside x reads row 0; its sums are dropped below
+      row = p.index[row];
+      row = row >= 0 && row < p.x_rows ? row : 0;
+    }
+    x[i] = p.rows + row * p.row_stride + g * 16;
+    if constexpr (TY == kGmmMX4) xs[i] = p.row_scales + row * p.blocks;
   }
 #pragma unroll
   for (int f = 0; f < FN; ++f) {
@@ -1210,14 +1209,8 @@ __global__ __launch_bounds__(512, MT <= 2 ? 4 : 2) void gmm_few(const GmmParams 
     w[f] = p.other + row * p.other_stride + g * 16;
     if constexpr (TY == kGmmMX4) ws[f] = p.other_scales + row * p.blocks;
   }
-  const bool scales4 = TY == kGmmMX4 &&
-                       ((reinterpret_cast<uintptr_t>(p.row_scales) |
-                         reinterpret_cast<uintptr_t>(p.other_scales) | uintptr_t(p.blocks)) & 3) == 0;
-  // The scale of this lane's chunk in step u, in the low byte.
-  auto scale = [&](const uint8_t* at, int step) -> int {
-    if (scales4) return int(reinterpret_cast<const uint32_t*>(at)[step] >> (8 * g));
-    return step * 4 + g < p.blocks ? at[step * 4 + g] : 0x7f;
-  };
+  // The scale of this lane's chunk in a step.
+  auto scale = [&](const uint8_t* at, int step) -> int { return at[step * 4 + g]; };
 
   float4v acc[MT][FN];
 #pragma unroll
@@ -1243,9 +1236,8 @@ __global__ __launch_bounds__(512, MT <= 2 ? 4 : 2) void gmm_few(const GmmParams 
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         xv[u][i] = int4v{0, 0, 0, 0};
-        if (have && real[i])
-          xv[u][i] = *reinterpret_cast<const int4v*>(x[i] + int64_t(first + u) * 64);
-        if constexpr (TY == kGmmMX4) xsv[u][i] = have && real[i] ? scale(xs[i], first + u) : 0x7f;
+        if (have) xv[u][i] = *reinterpret_cast<const int4v*>(x[i] + int64_t(first + u) * 64);
+        if constexpr (TY == kGmmMX4) xsv[u][i] = have ? scale(xs[i], first + u) : 0x7f;
       }
     }
 #pragma unroll
@@ -1276,13 +1268,20 @@ __global__ __launch_bounds__(512, MT <= 2 ? 4 : 2) void gmm_few(const GmmParams 
       *reinterpret_cast<float4v*>(&part[wave][i * FN + f][lane * 4]) = acc[i][f];
   __syncthreads();
   // Element (r, c): column c % 16 = 4g + j of fragment (r / 16, c / 16), lane 16 g + r % 16.
-  for (int q = tid; q < BM * BN; q += 512) {
+  for (int q = tid; q < BM * BN; q += NW * 64) {
     const int r = q / BN, c = q % BN;
     if (r >= t.rm || c >= t.cn) continue;
     const int at = ((c & 15) >> 2) * 64 + (r & 15) * 4 + (c & 3);
     float v = 0.0f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) v += part[i][(r >> 4) * FN + (c >> 4)][at];
+    if (p.index) {
+      const int64_t row = p.index[t.span.row0 + r];
+      if (row < 0 || row >= p.x_rows) {
+        v = 0.0f;
+        if (p.status) *p.status = A2AV_ERR_INVALID_ARGS;
+      }
+    }
     const int64_t o = (t.out_row0 + r) * p.out_stride + t.c0 + c;
     if (p.out_type == A2AV_FP32)
       reinterpret_cast<float*>(p.out)[o] = v;
@@ -1315,11 +1314,14 @@ hipError_t launch_tiles(Kernel kernel, int threads, const GmmParams& p, hipStrea
 template <int TY, int MODE>
 hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
   if constexpr (MODE == kGmmFwd) {
-    // By the mean rows of an expert (the counts stay on the device).
-    if (direct && p.nrows <= int64_t(p.E) * 12)
-      return launch_tiles<MODE, 16, 32>(gmm_few<TY, 1, 2>, 512, p, stream);
-    if (direct && p.nrows <= int64_t(p.E) * 40)
-      return launch_tiles<MODE, 32, 32>(gmm_few<TY, 2, 2>, 512, p, stream);
+    // By the mean rows of an expert (the counts stay on the device).  A row of 4
+    // bits is a quarter as long: fewer waves share it out.
+    constexpr int kWaves = TY == kGmmMX4 ? 4 : 8;
+    const bool rows = p.x_rows > 0;  // the streaming kernel reads row 0 for rows outside x
+    if (direct && rows && p.nrows <= int64_t(p.E) * 12)
+      return launch_tiles<MODE, 16, 32>(gmm_few<TY, 1, 2, kWaves>, kWaves * 64, p, stream);
+    if (direct && rows && p.nrows <= int64_t(p.E) * 40)
+      return launch_tiles<MODE, 32, 32>(gmm_few<TY, 2, 2, kWaves>, kWaves * 64, p, stream);
   }
   if (direct) {
     const int64_t cols = MODE == kGmmFwd ? p.N : p.K;
