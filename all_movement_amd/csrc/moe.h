@@ -43,7 +43,8 @@ struct RouteParams {
   int32_t* counts;
   int32_t* order;
   int32_t* place;
-  int32_t* hist;           // workspace [blocks][E]
+  int32_t* hist;           // workspace [E][blocks]
+  int32_t per_block;       // tokens of a block (set by launch_route)
 };
 
 struct RouteBackParams {
@@ -82,16 +83,31 @@ struct Mx4Params {
 };
 
 hipError_t launch_gmm(const GmmParams& p, GmmType type, GmmMode mode, hipStream_t stream);
-hipError_t launch_route(const RouteParams& p, hipStream_t stream);
+hipError_t launch_route(RouteParams p, hipStream_t stream);
 hipError_t launch_route_back(const RouteBackParams& p, hipStream_t stream);
 hipError_t launch_combine(const CombineParams& p, hipStream_t stream);
 hipError_t launch_combine_back(const CombineParams& p, hipStream_t stream);
 hipError_t launch_mx4_quantize(const Mx4Params& p, hipStream_t stream);
 hipError_t launch_mx4_dequantize(const Mx4Params& p, hipStream_t stream);
 
-// Tokens that one workgroup of the router's first kernel takes.
-constexpr int kRouteTokens = 64;
-// Up to this many slots the router is one workgroup and needs no workspace.
-constexpr int kRouteSmall = 1024;
+// The router's blocks: tokens of one workgroup of its first kernel, 8 to 64, so
+// that there are 256 blocks (one per CU) as soon as there are tokens for it.
+constexpr int kRouteMost = 64;
+inline int32_t route_per_block(int64_t tokens) {
+  const int64_t n = (tokens / 256 + 7) / 8 * 8;
+  return int32_t(n < 8 ? 8 : n > kRouteMost ? kRouteMost : n);
+}
+inline int32_t route_blocks(int64_t tokens) {
+  const int32_t n = route_per_block(tokens);
+  return int32_t((tokens + n - 1) / n);
+}
+// Few tokens: one workgroup does everything and needs no workspace.  Against the
+// three launches (k = 2): 64 experts, 32 tokens 5.3 us and 7.5, 128 tokens 13.8
+// and 8.3; 256 experts 7.4 and 8.5, 19.4 and 9.3; 512 experts, 16 tokens 11.0
+// and 12.1, 32 tokens 17.6 and 12.4.
+constexpr int kRouteSmall = 1024;  // slots
+inline bool route_is_small(int64_t tokens, int32_t E, int32_t k) {
+  return tokens * k <= kRouteSmall && tokens <= (E <= 64 ? 64 : E <= 256 ? 48 : 16);
+}
 
 }  // namespace a2av

@@ -1218,6 +1218,13 @@ __global__ __launch_bounds__(NW * 64, 4) void gmm_few(const GmmParams p) {
 #pragma unroll
     for (int f = 0; f < FN; ++f) acc[i][f] = float4v{0, 0, 0, 0};
 
+  // 16 bytes of a row, at any address, of which n elements exist.
+  auto load = [&](const uint8_t* from, int n) -> int4v {
+    if constexpr (TY == kGmmMX4)
+      return n > 0 ? *reinterpret_cast<const int4v*>(from) : int4v{0, 0, 0, 0};
+    else
+      return load_part(from, n);
+  };
   // Steps first .. first + n of 64 bytes; TAIL: some may lie past the end.
   auto run = [&](int first, auto n, auto tail) {
     constexpr int kN = decltype(n)::value;
@@ -1225,19 +1232,17 @@ __global__ __launch_bounds__(NW * 64, 4) void gmm_few(const GmmParams p) {
     int wsv[kN][FN], xsv[kN][MT];
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
-      const bool have =
-          !decltype(tail)::value || (first + u) * kStep + g * kPerChunk < K;
+      const int left =
+          decltype(tail)::value ? K - (first + u) * kStep - g * kPerChunk : kPerChunk;
 #pragma unroll
       for (int f = 0; f < FN; ++f) {
-        wv[u][f] = int4v{0, 0, 0, 0};
-        if (have) wv[u][f] = *reinterpret_cast<const int4v*>(w[f] + int64_t(first + u) * 64);
-        if constexpr (TY == kGmmMX4) wsv[u][f] = have ? scale(ws[f], first + u) : 0x7f;
+        wv[u][f] = load(w[f] + int64_t(first + u) * 64, left);
+        if constexpr (TY == kGmmMX4) wsv[u][f] = left > 0 ? scale(ws[f], first + u) : 0x7f;
       }
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        xv[u][i] = int4v{0, 0, 0, 0};
-        if (have) xv[u][i] = *reinterpret_cast<const int4v*>(x[i] + int64_t(first + u) * 64);
-        if constexpr (TY == kGmmMX4) xsv[u][i] = have ? scale(xs[i], first + u) : 0x7f;
+        xv[u][i] = load(x[i] + int64_t(first + u) * 64, left);
+        if constexpr (TY == kGmmMX4) xsv[u][i] = left > 0 ? scale(xs[i], first + u) : 0x7f;
       }
     }
 #pragma unroll
@@ -1318,9 +1323,9 @@ hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
     // bits is a quarter as long: fewer waves share it out.
     constexpr int kWaves = TY == kGmmMX4 ? 4 : 8;
     const bool rows = p.x_rows > 0;  // the streaming kernel reads row 0 for rows outside x
-    if (direct && rows && p.nrows <= int64_t(p.E) * 12)
+    if (rows && p.nrows <= int64_t(p.E) * 12)
       return launch_tiles<MODE, 16, 32>(gmm_few<TY, 1, 2, kWaves>, kWaves * 64, p, stream);
-    if (direct && rows && p.nrows <= int64_t(p.E) * 40)
+    if (rows && p.nrows <= int64_t(p.E) * 40)
       return launch_tiles<MODE, 32, 32>(gmm_few<TY, 2, 2, kWaves>, kWaves * 64, p, stream);
   }
   if (direct) {

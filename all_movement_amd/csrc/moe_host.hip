@@ -70,10 +70,6 @@ bool bad_gmm_sizes(int64_t x_rows, int64_t rows, int32_t E, int64_t N, int64_t K
          bad_size(K, 1) || N * K > (int64_t(1) << 58) / E || (!index && x_rows < rows);
 }
 
-int32_t route_blocks(int64_t tokens) {
-  return int32_t((tokens + kRouteTokens - 1) / kRouteTokens);
-}
-
 int check_route_sizes(int64_t tokens, int32_t E, int32_t k) {
   if (tokens < 0 || E < 1 || E > 1024 || k < 1 || k > 16 || k > E) return A2AV_ERR_INVALID_ARGS;
   return tokens > kMax31 / k ? A2AV_ERR_INVALID_ARGS : A2AV_OK;
@@ -87,7 +83,7 @@ int a2av_moe_route_workspace(int64_t tokens, int32_t E, int32_t k, int64_t* byte
   if (!bytes) return A2AV_ERR_NULLPTR;
   const int st = check_route_sizes(tokens, E, k);
   if (st != A2AV_OK) return st;
-  *bytes = tokens * k <= kRouteSmall ? 0 : int64_t(route_blocks(tokens)) * E * 4;
+  *bytes = route_is_small(tokens, E, k) ? 0 : int64_t(route_blocks(tokens)) * E * 4;
   return A2AV_OK;
 }
 

@@ -7,8 +7,8 @@
 //   (slots of smaller experts) + (slots of its expert in earlier blocks)
 //   + (those earlier in its block),
 // the last from a match of expert numbers inside a wave and a scan over the
-// block's waves, without atomics.  Up to kRouteSmall slots one workgroup does
-// all of it; past that three launches do (choose, scan, place).
+// block's waves, without atomics.  For few tokens one workgroup does all of it;
+// past that three launches do (choose, scan, place).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -342,18 +342,18 @@ __global__ __launch_bounds__(kThreads) void route_small(const RouteParams p) {
   }
 }
 
-// Choose: kRouteTokens tokens; the slots' ranks in the block go to place, the
+// Choose: p.per_block tokens; the slots' ranks in the block go to place, the
 // block's counts to hist[e][block].
 template <int PER>
 __global__ __launch_bounds__(kThreads) void route_choose(const RouteParams p, int blocks) {
-  __shared__ int32_t ids[kRouteTokens * 16];
+  __shared__ int32_t ids[kRouteMost * 16];
   __shared__ uint16_t hist[kWaves][kMaxE];
   __shared__ int32_t run[kMaxE];
   const int tid = threadIdx.x, wave = tid >> 6;
   const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
   for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const int t0 = b * kRouteTokens;
-    const int nt = p.tokens - t0 < kRouteTokens ? p.tokens - t0 : kRouteTokens;
+    const int t0 = b * p.per_block;
+    const int nt = p.tokens - t0 < p.per_block ? p.tokens - t0 : p.per_block;
     // The next token's logits are on their way while one is chosen from.
     Row<PER> row, next;
     if (wave < nt) next.load(p.logits, (t0 + wave) * p.stride, p.E, p.dtype, vec);
@@ -395,8 +395,8 @@ __global__ __launch_bounds__(kThreads) void route_place(const RouteParams p, int
   for (int i = tid; i < p.E; i += kThreads) first[i] = p.counts[i];
   const int all = first_rows(first, p.E);
   for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const int t0 = b * kRouteTokens;
-    const int nt = p.tokens - t0 < kRouteTokens ? p.tokens - t0 : kRouteTokens;
+    const int t0 = b * p.per_block;
+    const int nt = p.tokens - t0 < p.per_block ? p.tokens - t0 : p.per_block;
     const int n = nt * p.k;
     for (int f = tid; f < n; f += kThreads) {
       const int64_t s = int64_t(t0) * p.k + f;
@@ -493,15 +493,16 @@ void with_per(int E, F f) {
 
 }  // namespace
 
-hipError_t launch_route(const RouteParams& p, hipStream_t stream) {
+hipError_t launch_route(RouteParams p, hipStream_t stream) {
   (void)hipGetLastError();
-  if (int64_t(p.tokens) * p.k <= kRouteSmall) {
+  p.per_block = route_per_block(p.tokens);
+  if (route_is_small(p.tokens, p.E, p.k)) {
     with_per(p.E, [&](auto per) {
       route_small<decltype(per)::value><<<dim3(1), dim3(kThreads), 0, stream>>>(p);
     });
     return hipGetLastError();
   }
-  const int blocks = (p.tokens + kRouteTokens - 1) / kRouteTokens;
+  const int blocks = route_blocks(p.tokens);
   const int grid = blocks < 65536 ? blocks : 65536;
   with_per(p.E, [&](auto per) {
     route_choose<decltype(per)::value><<<dim3(grid), dim3(kThreads), 0, stream>>>(p, blocks);

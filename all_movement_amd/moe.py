@@ -16,7 +16,9 @@ tensor of one element, receives the code of a check on device data that failed
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -69,18 +71,21 @@ def _matrix(t, name: str, cols: int | None = None, dtypes=None):
     """A 2-D tensor with contiguous rows: (pointer, row stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {len(shape)}")
     if dtypes is not None and t.dtype not in dtypes:
-        raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if cols is not None and t.shape[1] != cols:
-        raise ValueError(f"{name} must have {cols} columns, got {t.shape[1]}")
-    rows, width = t.shape
-    stride = t.stride(0) if rows > 1 else max(width, 1)
-    if width > 1 and t.stride(1) != 1 or rows > 1 and stride < width:
+        raise ValueError(f"{name} must be one of {tuple(dtypes)}, got {t.dtype}")
+    rows, width = shape
+    if cols is not None and width != cols:
+        raise ValueError(f"{name} must have {cols} columns, got {width}")
+    along, step = t.stride()
+    if rows <= 1:
+        along = width if width > 1 else 1
+    if width > 1 and step != 1 or along < width:
         raise ValueError(f"{name} must have contiguous rows that do not overlap "
                          "(operands are never copied)")
-    return t.data_ptr(), stride
+    return t.data_ptr(), along
 
 
 def _whole(t, name: str, shape, dtype):
@@ -89,7 +94,7 @@ def _whole(t, name: str, shape, dtype):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (operands are never copied)")
@@ -99,41 +104,28 @@ def _whole(t, name: str, shape, dtype):
 def _device(*named):
     dev = named[0].device
     for t in named:
-        if t is not None and t.device != dev:
+        if t is not None and t is not named[0] and t.device != dev:
             raise ValueError(f"operands on {dev} and {t.device}")
     if dev.type != "cuda":
         raise ValueError(f"operands must live on a GPU, not {dev}")
     return dev
 
 
-class _On:
-    """The tensors' device made current, and the stream there."""
+def _elsewhere(dev, stream) -> bool:
+    """Whether the call has to be made under another device or stream."""
+    return stream is not None or torch._C._cuda_getDevice() != dev.index
 
-    __slots__ = ("dev", "before", "given", "stream", "scope")
 
-    def __init__(self, dev, stream):
-        self.dev = dev.index
-        self.given = stream
+@contextlib.contextmanager
+def _there(dev, stream):
+    """The tensors' device made current, and the stream on it."""
+    with torch.cuda.device(dev):
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+            yield
 
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.dev:
-            torch.cuda.set_device(self.dev)
-        self.scope = None
-        if self.given is not None:
-            self.scope = torch.cuda.stream(self.given)
-            self.scope.__enter__()
-            self.stream = self.given.cuda_stream
-        else:
-            self.stream = torch._C._cuda_getCurrentRawStream(self.dev)
-        return self
 
-    def __exit__(self, *e):
-        if self.scope is not None:
-            self.scope.__exit__(*e)
-        if self.before != self.dev:
-            torch.cuda.set_device(self.before)
-        return False
+def _stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _status(status, check: bool, dev):
@@ -161,6 +153,7 @@ class Routing(NamedTuple):
     place: torch.Tensor    # int32 [tokens, k]: the row of each slot, -1 = none
 
 
+@functools.lru_cache(maxsize=256)
 def route_workspace(tokens: int, experts: int, k: int) -> int:
     """Bytes of workspace that :func:`route` needs."""
     n = ctypes.c_int64()
@@ -176,27 +169,33 @@ def route(logits, k: int, *, renormalize: bool = True, out: Routing | None = Non
     T, E = logits.shape
     need = route_workspace(T, E, k)
     dev = _device(logits, workspace, *(out or ()))
-    with _On(dev, stream) as on:
-        if out is None:
-            ints = torch.empty(3 * T * k + E, dtype=torch.int32, device=dev)
-            n = T * k
-            out = Routing(ints[:n].view(T, k), torch.empty(T, k, dtype=torch.float32, device=dev),
-                          ints[3 * n:], ints[n:2 * n], ints[2 * n:3 * n].view(T, k))
-        ptr = [_whole(out[0], "experts", (T, k), torch.int32),
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return route(logits, k, renormalize=renormalize, out=out, workspace=workspace)
+    n = T * k
+    if out is None:
+        ints = torch.empty(3, T, k, dtype=torch.int32, device=dev)
+        experts, order, place = ints.unbind(0)
+        weights = torch.empty(T, k, dtype=torch.float32, device=dev)
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        out = Routing(experts, weights, counts, order.view(n), place)
+        i = ints.data_ptr()
+        ptr = (i, weights.data_ptr(), counts.data_ptr(), i + 4 * n, i + 8 * n)
+    else:
+        ptr = (_whole(out[0], "experts", (T, k), torch.int32),
                _whole(out[1], "weights", (T, k), torch.float32),
                _whole(out[2], "counts", (E,), torch.int32),
-               _whole(out[3], "order", (T * k,), torch.int32),
-               _whole(out[4], "place", (T, k), torch.int32)]
-        wp, wn = None, 0
-        if need:
-            if workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            wn = workspace.numel() * workspace.element_size()
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be contiguous")
-            wp = workspace.data_ptr()
-        st = lib().a2av_moe_route(p, stride, T, E, k, int(renormalize), _DTYPE[logits.dtype], *ptr,
-                                  wp, wn, on.stream)
+               _whole(out[3], "order", (n,), torch.int32),
+               _whole(out[4], "place", (T, k), torch.int32))
+    wp, wn = None, 0
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = lib().a2av_moe_route(p, stride, T, E, k, int(renormalize), _DTYPE[logits.dtype], *ptr,
+                              wp, wn, _stream(dev))
     a2av._raise(st, "a2av_moe_route")
     return out
 
@@ -209,15 +208,18 @@ def route_backward(logits, experts, weights, dweights, *, renormalize: bool = Tr
     T, E = logits.shape
     k = experts.shape[-1]
     dev = _device(logits, experts, weights, dweights, out)
-    ptr = [_whole(experts, "experts", (T, k), torch.int32),
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return route_backward(logits, experts, weights, dweights, renormalize=renormalize,
+                                  out=out)
+    ptr = (_whole(experts, "experts", (T, k), torch.int32),
            _whole(weights, "weights", (T, k), torch.float32),
-           _whole(dweights, "dweights", (T, k), torch.float32)]
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty(T, E, dtype=logits.dtype, device=dev)
-        op = _whole(out, "out", (T, E), logits.dtype)
-        st = lib().a2av_moe_route_backward(p, stride, T, E, k, int(renormalize),
-                                           _DTYPE[logits.dtype], *ptr, op, on.stream)
+           _whole(dweights, "dweights", (T, k), torch.float32))
+    if out is None:
+        out = torch.empty(T, E, dtype=logits.dtype, device=dev)
+    op = _whole(out, "out", (T, E), logits.dtype)
+    st = lib().a2av_moe_route_backward(p, stride, T, E, k, int(renormalize), _DTYPE[logits.dtype],
+                                       *ptr, op, _stream(dev))
     a2av._raise(st, "a2av_moe_route_backward")
     return out
 
@@ -227,6 +229,17 @@ def route_backward(logits, experts, weights, dweights, *, renormalize: bool = Tr
 def _grouped(counts, index, E: int, rows: int):
     cp = _whole(counts, "counts", (E,), torch.int32)
     return cp, None if index is None else _whole(index, "index", (rows,), torch.int32)
+
+
+def _rows_out(out, rows: int, cols: int, dtype, dev, name: str = "out"):
+    """``out`` or a new [rows, cols] tensor: (tensor, pointer, row stride)."""
+    if out is None:
+        out = torch.empty(rows, cols, dtype=dtype, device=dev)
+        return out, out.data_ptr(), max(cols, 1)
+    p, stride = _matrix(out, name, cols, (dtype,))
+    if out.shape[0] != rows:
+        raise ValueError(f"{name} must have {rows} rows, got {out.shape[0]}")
+    return out, p, stride
 
 
 def gmm(x, w, counts, *, index=None, out=None, status=None, check: bool = False, stream=None):
@@ -244,16 +257,14 @@ def gmm(x, w, counts, *, index=None, out=None, status=None, check: bool = False,
     rows = x.shape[0] if index is None else index.numel()
     cp, ip = _grouped(counts, index, E, rows)
     dev = _device(x, w, counts, index, out, status)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty(rows, N, dtype=x.dtype, device=dev)
-        op, os = _matrix(out, "out", N, (x.dtype,))
-        if out.shape[0] != rows:
-            raise ValueError(f"out must have {rows} rows, got {out.shape[0]}")
-        status, sp = _status(status, check, dev)
-        st = lib().a2av_moe_gmm(xp, xs, x.shape[0], wp, cp, ip, op, os, rows, E, N, K,
-                                _DTYPE[x.dtype], sp, on.stream)
-        _done(st, "a2av_moe_gmm", status, check)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gmm(x, w, counts, index=index, out=out, status=status, check=check)
+    out, op, os = _rows_out(out, rows, N, x.dtype, dev)
+    status, sp = _status(status, check, dev)
+    st = lib().a2av_moe_gmm(xp, xs, x.shape[0], wp, cp, ip, op, os, rows, E, N, K,
+                            _DTYPE[x.dtype], sp, _stream(dev))
+    _done(st, "a2av_moe_gmm", status, check)
     return out
 
 
@@ -269,16 +280,14 @@ def gmm_dx(dy, w, counts, *, out=None, status=None, check: bool = False, stream=
     wp = _whole(w, "w", (E, N, K), dy.dtype)
     cp, _ = _grouped(counts, None, E, rows)
     dev = _device(dy, w, counts, out, status)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty(rows, K, dtype=dy.dtype, device=dev)
-        op, os = _matrix(out, "out", K, (dy.dtype,))
-        if out.shape[0] != rows:
-            raise ValueError(f"out must have {rows} rows, got {out.shape[0]}")
-        status, sp = _status(status, check, dev)
-        st = lib().a2av_moe_gmm_dx(yp, ys, wp, cp, op, os, rows, E, N, K, _DTYPE[dy.dtype], sp,
-                                   on.stream)
-        _done(st, "a2av_moe_gmm_dx", status, check)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gmm_dx(dy, w, counts, out=out, status=status, check=check)
+    out, op, os = _rows_out(out, rows, K, dy.dtype, dev)
+    status, sp = _status(status, check, dev)
+    st = lib().a2av_moe_gmm_dx(yp, ys, wp, cp, op, os, rows, E, N, K, _DTYPE[dy.dtype], sp,
+                               _stream(dev))
+    _done(st, "a2av_moe_gmm_dx", status, check)
     return out
 
 
@@ -293,37 +302,45 @@ def gmm_dw(dy, x, counts, *, index=None, out=None, out_dtype=None, status=None,
     if out_dtype is None:
         out_dtype = dy.dtype if out is None else out.dtype
     dev = _device(dy, x, counts, index, out, status)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty(E, N, K, dtype=out_dtype, device=dev)
-        op = _whole(out, "out", (E, N, K), out_dtype)
-        status, sp = _status(status, check, dev)
-        st = lib().a2av_moe_gmm_dw(yp, ys, xp, xs, x.shape[0], cp, ip, op, rows, E, N, K,
-                                   _DTYPE[dy.dtype], _DTYPE.get(out_dtype, -1), sp, on.stream)
-        _done(st, "a2av_moe_gmm_dw", status, check)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gmm_dw(dy, x, counts, index=index, out=out, out_dtype=out_dtype, status=status,
+                          check=check)
+    if out is None:
+        out = torch.empty(E, N, K, dtype=out_dtype, device=dev)
+    op = _whole(out, "out", (E, N, K), out_dtype)
+    status, sp = _status(status, check, dev)
+    st = lib().a2av_moe_gmm_dw(yp, ys, xp, xs, x.shape[0], cp, ip, op, rows, E, N, K,
+                               _DTYPE[dy.dtype], _DTYPE.get(out_dtype, -1), sp, _stream(dev))
+    _done(st, "a2av_moe_gmm_dw", status, check)
     return out
 
 
 # ---------------------------------------------------------------- the weighted return
 
+def _slots(place, weights):
+    if place.dim() != 2:
+        raise ValueError(f"place must be [tokens, k], got {tuple(place.shape)}")
+    T, k = place.shape
+    pp = _whole(place, "place", (T, k), torch.int32)
+    return T, k, pp, None if weights is None else _whole(weights, "weights", (T, k), torch.float32)
+
+
 def combine(y, place, weights=None, *, out=None, status=None, check: bool = False, stream=None):
     """out[t] = sum over j of weights[t, j] * y[place[t, j]]; slots of -1 are left
     out, without ``weights`` each counts once."""
     yp, ys = _matrix(y, "y", None, _DTYPE)
-    T, k = place.shape
-    pp = _whole(place, "place", (T, k), torch.int32)
-    wp = None if weights is None else _whole(weights, "weights", (T, k), torch.float32)
+    T, k, pp, wp = _slots(place, weights)
     dev = _device(y, place, weights, out, status)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty(T, y.shape[1], dtype=y.dtype, device=dev)
-        op, os = _matrix(out, "out", y.shape[1], (y.dtype,))
-        if out.shape[0] != T:
-            raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
-        status, sp = _status(status, check, dev)
-        st = lib().a2av_moe_combine(yp, ys, y.shape[0], pp, wp, op, os, T, k, y.shape[1],
-                                    _DTYPE[y.dtype], sp, on.stream)
-        _done(st, "a2av_moe_combine", status, check)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return combine(y, place, weights, out=out, status=status, check=check)
+    rows, width = y.shape
+    out, op, os = _rows_out(out, T, width, y.dtype, dev)
+    status, sp = _status(status, check, dev)
+    st = lib().a2av_moe_combine(yp, ys, rows, pp, wp, op, os, T, k, width, _DTYPE[y.dtype], sp,
+                                _stream(dev))
+    _done(st, "a2av_moe_combine", status, check)
     return out
 
 
@@ -333,25 +350,25 @@ def combine_backward(dout, y, place, weights=None, *, out=None, status=None, che
     Rows of dy that no slot names are not written."""
     dp, ds = _matrix(dout, "dout", None, _DTYPE)
     yp, ys = _matrix(y, "y", dout.shape[1], (dout.dtype,))
-    T, k = place.shape
+    T, k, pp, wp = _slots(place, weights)
     if dout.shape[0] != T:
         raise ValueError(f"dout must have {T} rows, got {dout.shape[0]}")
-    pp = _whole(place, "place", (T, k), torch.int32)
-    wp = None if weights is None else _whole(weights, "weights", (T, k), torch.float32)
     dev = _device(dout, y, place, weights, status, *(out or ()))
-    with _On(dev, stream) as on:
-        if out is None:
-            out = (torch.empty(y.shape, dtype=y.dtype, device=dev),
-                   None if weights is None else torch.empty(T, k, dtype=torch.float32, device=dev))
-        op, os = _matrix(out[0], "dy", y.shape[1], (y.dtype,))
-        if out[0].shape[0] != y.shape[0]:
-            raise ValueError(f"dy must have {y.shape[0]} rows, got {out[0].shape[0]}")
-        gp = None if out[1] is None else _whole(out[1], "dweights", (T, k), torch.float32)
-        status, sp = _status(status, check, dev)
-        st = lib().a2av_moe_combine_backward(dp, ds, yp, ys, y.shape[0], pp, wp, op, os, gp, T, k,
-                                             y.shape[1], _DTYPE[y.dtype], sp, on.stream)
-        _done(st, "a2av_moe_combine_backward", status, check)
-    return out
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return combine_backward(dout, y, place, weights, out=out, status=status, check=check)
+    rows, width = y.shape
+    dy, op, os = _rows_out(None if out is None else out[0], rows, width, y.dtype, dev, "dy")
+    if out is None:
+        dw = None if weights is None else torch.empty(T, k, dtype=torch.float32, device=dev)
+    else:
+        dw = out[1]
+    gp = None if dw is None else _whole(dw, "dweights", (T, k), torch.float32)
+    status, sp = _status(status, check, dev)
+    st = lib().a2av_moe_combine_backward(dp, ds, yp, ys, rows, pp, wp, op, os, gp, T, k, width,
+                                         _DTYPE[y.dtype], sp, _stream(dev))
+    _done(st, "a2av_moe_combine_backward", status, check)
+    return dy, dw
 
 
 # ---------------------------------------------------------------- 4-bit rows
@@ -363,14 +380,16 @@ def mx4_quantize(x, *, out=None, stream=None):
     rows, cols = x.shape
     B = (cols + 31) // 32
     dev = _device(x, *(out or ()))
-    with _On(dev, stream) as on:
-        if out is None:
-            out = (torch.empty(rows, B * 16, dtype=torch.uint8, device=dev),
-                   torch.empty(rows, B, dtype=torch.uint8, device=dev))
-        st = lib().a2av_moe_mx4_quantize(p, stride, rows, cols, _DTYPE[x.dtype],
-                                         _whole(out[0], "codes", (rows, B * 16), torch.uint8),
-                                         _whole(out[1], "scales", (rows, B), torch.uint8),
-                                         on.stream)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return mx4_quantize(x, out=out)
+    if out is None:
+        out = (torch.empty(rows, B * 16, dtype=torch.uint8, device=dev),
+               torch.empty(rows, B, dtype=torch.uint8, device=dev))
+    st = lib().a2av_moe_mx4_quantize(p, stride, rows, cols, _DTYPE[x.dtype],
+                                     _whole(out[0], "codes", (rows, B * 16), torch.uint8),
+                                     _whole(out[1], "scales", (rows, B), torch.uint8),
+                                     _stream(dev))
     a2av._raise(st, "a2av_moe_mx4_quantize")
     return out
 
@@ -381,14 +400,12 @@ def mx4_dequantize(codes, scales, cols: int, dtype=torch.bfloat16, *, out=None, 
     cp = _whole(codes, "codes", (rows, B * 16), torch.uint8)
     sp = _whole(scales, "scales", (rows, B), torch.uint8)
     dev = _device(codes, scales, out)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty(rows, cols, dtype=dtype, device=dev)
-        op, os = _matrix(out, "out", cols, (dtype,))
-        if out.shape[0] != rows:
-            raise ValueError(f"out must have {rows} rows, got {out.shape[0]}")
-        st = lib().a2av_moe_mx4_dequantize(cp, sp, rows, cols, _DTYPE.get(dtype, -1), op, os,
-                                           on.stream)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return mx4_dequantize(codes, scales, cols, dtype, out=out)
+    out, op, os = _rows_out(out, rows, cols, dtype, dev)
+    st = lib().a2av_moe_mx4_dequantize(cp, sp, rows, cols, _DTYPE.get(dtype, -1), op, os,
+                                       _stream(dev))
     a2av._raise(st, "a2av_moe_mx4_dequantize")
     return out
 
@@ -402,21 +419,20 @@ def gmm_mx4(x_codes, x_scales, w_codes, w_scales, counts, *, index=None, dtype=t
         raise ValueError(f"w_scales must be [experts, N, blocks], got {tuple(w_scales.shape)}")
     E, N, B = w_scales.shape
     x_rows = x_scales.shape[0]
-    ptr = [_whole(x_codes, "x_codes", (x_rows, B * 16), torch.uint8),
+    ptr = (_whole(x_codes, "x_codes", (x_rows, B * 16), torch.uint8),
            _whole(x_scales, "x_scales", (x_rows, B), torch.uint8), x_rows,
            _whole(w_codes, "w_codes", (E, N, B * 16), torch.uint8),
-           _whole(w_scales, "w_scales", (E, N, B), torch.uint8)]
+           _whole(w_scales, "w_scales", (E, N, B), torch.uint8))
     rows = x_rows if index is None else index.numel()
     cp, ip = _grouped(counts, index, E, rows)
     dev = _device(x_codes, x_scales, w_codes, w_scales, counts, index, out, status)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty(rows, N, dtype=dtype, device=dev)
-        op, os = _matrix(out, "out", N, (dtype,))
-        if out.shape[0] != rows:
-            raise ValueError(f"out must have {rows} rows, got {out.shape[0]}")
-        status, sp = _status(status, check, dev)
-        st = lib().a2av_moe_gmm_mx4(*ptr, cp, ip, op, os, rows, E, N, B * 32,
-                                    _DTYPE.get(dtype, -1), sp, on.stream)
-        _done(st, "a2av_moe_gmm_mx4", status, check)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gmm_mx4(x_codes, x_scales, w_codes, w_scales, counts, index=index, dtype=dtype,
+                           out=out, status=status, check=check)
+    out, op, os = _rows_out(out, rows, N, dtype, dev)
+    status, sp = _status(status, check, dev)
+    st = lib().a2av_moe_gmm_mx4(*ptr, cp, ip, op, os, rows, E, N, B * 32, _DTYPE.get(dtype, -1),
+                                sp, _stream(dev))
+    _done(st, "a2av_moe_gmm_mx4", status, check)
     return out
