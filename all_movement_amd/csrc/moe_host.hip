@@ -61,7 +61,9 @@ bool bad_addresses(std::initializer_list<Operand> all) {
 
 int launched(hipError_t e) { return e == hipSuccess ? A2AV_OK : A2AV_ERR_HIP; }
 
-bool bad_size(int64_t v, int64_t least) { return v < least || v > kMax31; }
+// Sizes stay a factor of two inside 32 bits: the kernels add a tile to them.
+constexpr int64_t kMostSize = int64_t(1) << 30;
+bool bad_size(int64_t v, int64_t least) { return v < least || v > kMostSize; }
 
 // The sizes that all grouped products check alike.
 bool bad_gmm_sizes(int64_t x_rows, int64_t rows, int32_t E, int64_t N, int64_t K,
@@ -72,7 +74,7 @@ bool bad_gmm_sizes(int64_t x_rows, int64_t rows, int32_t E, int64_t N, int64_t K
 
 int check_route_sizes(int64_t tokens, int32_t E, int32_t k) {
   if (tokens < 0 || E < 1 || E > 1024 || k < 1 || k > 16 || k > E) return A2AV_ERR_INVALID_ARGS;
-  return tokens > kMax31 / k ? A2AV_ERR_INVALID_ARGS : A2AV_OK;
+  return tokens > kMostSize / k ? A2AV_ERR_INVALID_ARGS : A2AV_OK;
 }
 
 }  // namespace

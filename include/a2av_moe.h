@@ -19,7 +19,8 @@
  *   - `status` is a device int32 that may be NULL.  The device writes it only
  *     when a check on device data fails (the codes of a2av.h), so it is a
  *     latch that the caller clears; the call itself has returned A2AV_OK.
- *   - Strides are in elements from one row to the next; rows are contiguous.
+ *   - Strides are in elements from one row to the next, below 2^31; rows are
+ *     contiguous.
  *   - Sums, softmax statistics and gradients of weights are held in FP32; a
  *     result is rounded once, to nearest even, to its type.  No result depends
  *     on the order in which workgroups run.
@@ -51,7 +52,7 @@ extern "C" {
  *   place[t][j]    the row of slot j, -1 for an empty one
  * A NaN logit ranks above every number (the lowest numbered first) and makes
  * the token's weights NaN, as softmax does; so does +inf.
- * Limits: tokens * k < 2^31, E in 1..1024, k in 1..min(E, 16).
+ * Limits: tokens * k <= 2^30, E in 1..1024, k in 1..min(E, 16).
  */
 
 /* Bytes of workspace that a2av_moe_route needs for these sizes (0 when it
@@ -96,7 +97,7 @@ int a2av_moe_route_backward(const void *logits, int64_t logits_stride, int64_t t
  * Device checks: a negative count, or counts that sum to more than `rows` ->
  * INVALID_ARGS, nothing written; an index in use outside [0, x_rows) ->
  * INVALID_ARGS, and that row counts as a row of zeros.
- * Limits: rows, x_rows, N, K < 2^31, E in 1..4096.
+ * Limits: rows, x_rows, N, K <= 2^30, E in 1..4096.
  */
 int a2av_moe_gmm(const void *x, int64_t x_stride, int64_t x_rows, const void *w,
                  const int32_t *counts, const int32_t *index, void *y, int64_t y_stride,
@@ -122,7 +123,7 @@ int a2av_moe_gmm_dw(const void *dy, int64_t dy_stride, const void *x, int64_t x_
  * Rows of dy that no slot names are not written; a row may be named by one
  * slot only (two leave one of the two values).  Device check: a place outside
  * [-1, y_rows) -> INVALID_ARGS, and the slot counts as empty.
- * Limits: tokens, y_rows, width < 2^31, k in 1..64.
+ * Limits: tokens, y_rows, width <= 2^30, k in 1..64.
  */
 int a2av_moe_combine(const void *y, int64_t y_stride, int64_t y_rows, const int32_t *place,
                      const float *weights, void *out, int64_t out_stride, int64_t tokens,
@@ -146,7 +147,7 @@ int a2av_moe_combine_backward(const void *dout, int64_t dout_stride, const void 
  * to even, magnitudes past 6 to 6; a zero keeps its sign.  A block with a NaN
  * or an infinity has s = 255 and codes 0.
  * dequantize: code * 2^(s - 127) rounded to dtype (past its range: infinity).
- * x FP32, FP16 or BF16.  Limits: rows, cols < 2^31; codes 16-byte aligned.
+ * x FP32, FP16 or BF16.  Limits: rows, cols <= 2^30; codes 16-byte aligned.
  */
 int a2av_moe_mx4_quantize(const void *x, int64_t x_stride, int64_t rows, int64_t cols,
                           int32_t dtype, uint8_t *codes, uint8_t *scales, void *stream);

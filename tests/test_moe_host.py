@@ -96,13 +96,13 @@ def test_dw_types():
 
 BAD = {
     "a2av_moe_route": [dict(tokens=-1), dict(E=0), dict(E=1025, stride=2000), dict(k=0), dict(k=17),
-                       dict(k=3, E=2), dict(stride=63), dict(tokens=2 ** 31), dict(tokens=2 ** 30),
+                       dict(k=3, E=2), dict(stride=63), dict(tokens=2 ** 31), dict(tokens=2 ** 30 + 1),
                        dict(tokens=5000, ws=A[8], ws_bytes=4), dict(logits=A[0] + 2),
                        dict(order=A[4] + 1), dict(experts=A[2] + 8), dict(place=A[0] + 400)],
     "a2av_moe_route_backward": [dict(E=1025, stride=2000), dict(k=65), dict(stride=3),
                                 dict(dlogits=A[0] + 4), dict(weights=A[2] + 2)],
     "a2av_moe_gmm": [dict(E=0), dict(E=4097), dict(N=0), dict(K=0), dict(rows=-1), dict(x_rows=9),
-                     dict(x_stride=63), dict(y_stride=31), dict(rows=2 ** 31, x_rows=2 ** 31),
+                     dict(x_stride=63), dict(y_stride=31), dict(rows=2 ** 30 + 1, x_rows=2 ** 30 + 1),
                      dict(y=A[0] + 100), dict(y=A[1] + 2), dict(x=A[0] + 1), dict(counts=A[2] + 2),
                      dict(status=A[3] + 4), dict(N=2 ** 31 - 1, K=2 ** 31 - 1, E=4096,
                                                  x_stride=2 ** 31 - 1, y_stride=2 ** 31 - 1)],
