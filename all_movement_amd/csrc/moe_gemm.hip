@@ -136,33 +136,34 @@ __device__ inline bool find_work(const GmmParams& p, Tile* t, int* part) {
       *p.status = A2AV_ERR_INVALID_ARGS;
     return false;
   }
-  const int64_t row_tiles = k.tiles_before + lane_value(k.tiles, 63);
-  const int64_t out_cols = MODE == kGmmFwd ? p.N : p.K;
-  const int64_t col_tiles = (out_cols + BN - 1) / BN;
-  const int64_t per_e = (p.N + BM - 1) / BM;  // dw: row tiles of an expert
-  const int64_t tm_all = MODE == kGmmDw ? int64_t(p.E) * per_e : row_tiles;
-  const int64_t total = tm_all * col_tiles;
-  const int64_t wg = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
-  const int64_t whole = total / 256 * 256, rest = total - whole;
+  // The host refuses products of 2^31 tiles and more.
+  const uint32_t row_tiles = uint32_t(k.tiles_before + lane_value(k.tiles, 63));
+  const uint32_t out_cols = MODE == kGmmFwd ? p.N : p.K;
+  const uint32_t col_tiles = (out_cols + BN - 1) / BN;
+  const uint32_t per_e = (uint32_t(p.N) + BM - 1) / BM;  // dw: row tiles of an expert
+  const uint32_t tm_all = MODE == kGmmDw ? uint32_t(p.E) * per_e : row_tiles;
+  const uint32_t total = tm_all * col_tiles;
+  const uint32_t wg = blockIdx.y * gridDim.x + blockIdx.x;
+  const uint32_t whole = total / 256 * 256, rest = total - whole;
   const bool cut = SPLIT && rest <= 128;
-  int64_t tile;
+  uint32_t tile;
   *part = -1;
   if (wg < whole) {
     tile = ((wg >> 8) * 8 + (wg & 7)) * 32 + (wg >> 3 & 31);
   } else {
-    const int64_t n = cut ? rest * 4 : rest, per = (n + 7) / 8;
-    const int64_t i = (wg - whole) >> 3, u = ((wg - whole) & 7) * per + i;
+    const uint32_t n = cut ? rest * 4 : rest, per = (n + 7) / 8;
+    const uint32_t i = (wg - whole) >> 3, u = ((wg - whole) & 7) * per + i;
     if (i >= per || u >= n) return false;
     tile = whole + (cut ? u >> 2 : u);
     if (cut) *part = int(u & 3);
   }
-  constexpr int kGroup = 4;
-  const int64_t grp = tile / (kGroup * col_tiles);
-  const int64_t in_grp = tile - grp * kGroup * col_tiles;
-  const int64_t grp_rows = tm_all - grp * kGroup < kGroup ? tm_all - grp * kGroup : kGroup;
-  const int64_t tm = grp * kGroup + in_grp % grp_rows;
-  const int64_t tn = in_grp / grp_rows;
-  const int want = MODE == kGmmDw ? int(tm / per_e) : 0;
+  constexpr uint32_t kGroup = 4;
+  const uint32_t grp = tile / (kGroup * col_tiles);
+  const uint32_t in_grp = tile - grp * kGroup * col_tiles;
+  const uint32_t grp_rows = tm_all - grp * kGroup < kGroup ? tm_all - grp * kGroup : kGroup;
+  const uint32_t tn = in_grp / grp_rows;
+  const uint32_t tm = grp * kGroup + (in_grp - tn * grp_rows);
+  const int want = MODE == kGmmDw ? int(tm / per_e) : 0;  // dw: the tile's expert
   int b = 0;
   if (p.E > 64) {  // the counts again, as far as the tile's expert
     k = Counts{};
@@ -175,7 +176,7 @@ __device__ inline bool find_work(const GmmParams& p, Tile* t, int* part) {
   }
   if constexpr (MODE == kGmmDw) {
     t->span = k.at(b, want - b);
-    t->out_row0 = (tm - want * per_e) * BM;
+    t->out_row0 = int64_t(tm - want * per_e) * BM;
     t->rm = int(p.N - t->out_row0 < BM ? p.N - t->out_row0 : BM);
   } else {
     const uint64_t past = __ballot(k.tiles_before + k.tiles > tm);
@@ -189,8 +190,8 @@ __device__ inline bool find_work(const GmmParams& p, Tile* t, int* part) {
     t->out_row0 = t->span.row0;
     t->rm = t->span.m;
   }
-  t->c0 = tn * BN;
-  t->cn = int(out_cols - t->c0 < BN ? out_cols - t->c0 : BN);
+  t->c0 = int64_t(tn) * BN;
+  t->cn = int(out_cols - tn * BN < BN ? out_cols - tn * BN : BN);
   if (*part >= 0) {
     const int r = (*part & 1) * (BM / 2), c = (*part >> 1) * (BN / 2);
     if (r >= t->rm || c >= t->cn) return false;
@@ -959,16 +960,19 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
     } else {
       const int j = i - kQ;
       const uint8_t* from = cbase + s * cstep;
-      uint32_t offset = co[j];
-      if constexpr (kGather) offset += uint32_t(next_row[j]) * uint32_t(p.other_stride);
+      if constexpr (kGather)
+        from += uint64_t(uint32_t(next_row[j])) * uint32_t(p.other_stride) + co[j];
+      else if constexpr (!decltype(fast)::value)
+        from += co[j];
       if constexpr (decltype(fast)::value) {
-        load_to_lds(from, offset, to);
+        if constexpr (kGather) load_to_lds(from, to);
+        else load_to_lds(from, co[j], to);
       } else {
         const int at = kColsAlong ? s * kStage + C::chunk(lane) * kPerChunk
                                   : s * 64 + (wave * kC + j) * C::kRows + C::row(lane);
         const bool have =
             at < red && (!kGather || (next_row[j] >= 0 && next_row[j] < p.x_rows));
-        load_to_lds(have ? from + offset : zeros, to);
+        load_to_lds(have ? from : zeros, to);
       }
     }
   };
@@ -1305,12 +1309,12 @@ hipError_t launch_tiles(Kernel kernel, int threads, const GmmParams& p, hipStrea
   const int64_t row_tiles = MODE == kGmmDw ? int64_t(p.E) * ((p.N + BM - 1) / BM)
                                            : (p.nrows + used * (BM - 1)) / BM;
   if (row_tiles * col_tiles <= 0) return hipSuccess;
+  if (row_tiles > 0x7fff0000 / col_tiles) return hipErrorInvalidConfiguration;
   // Quarters of up to 128 tiles come on top.
   const int64_t grid = (row_tiles * col_tiles + (BM == 256 ? 3 * 128 : 0) + 7) / 8 * 8;
   // A launch's threads have to stay below 2^32 in x: long ones go on in y.
   const int64_t gx = grid < (1 << 20) ? grid : (1 << 20);
   const int64_t gy = (grid + gx - 1) / gx;
-  if (gy > 65535) return hipErrorInvalidConfiguration;
   (void)hipGetLastError();
   kernel<<<dim3(uint32_t(gx), uint32_t(gy)), dim3(uint32_t(threads)), 0, stream>>>(p);
   return hipGetLastError();
@@ -1359,14 +1363,16 @@ hipError_t launch_gmm(const GmmParams& p, GmmType type, GmmMode mode, hipStream_
   // The loads to LDS move aligned chunks of 16 bytes: every row has to begin
   // and end on one.
   const uintptr_t bases = reinterpret_cast<uintptr_t>(p.rows) | reinterpret_cast<uintptr_t>(p.other);
-  // They go by 32-bit offsets from a tile's first row (x that is gathered: from
-  // its first).  Anything else takes the kernel with plain loads.
+  // They go by 32-bit offsets from a tile's first row (x that the forward product
+  // gathers: from its first; the weight gradient's x by 64 bits).  Anything else
+  // takes the kernel with plain loads.
   const int64_t far = (int64_t(1) << 32) - 256;
-  const bool all_x = mode == kGmmDw || (mode == kGmmFwd && p.index);
-  const int64_t x_stride = mode == kGmmDw ? p.other_stride : p.row_stride;
+  const bool all_x = mode == kGmmFwd && p.index;
+  const int chunked = mode == kGmmFwd ? p.K : p.N | p.K;  // widths that loads run along
   const bool direct = ((bases | uint64_t(p.row_stride) | uint64_t(p.other_stride)) & 15) == 0 &&
-                      ((p.N | p.K) & 7) == 0 && p.row_stride <= far / 256 &&
-                      p.other_stride <= far / 256 && (!all_x || x_stride <= far / (p.x_rows + 1));
+                      (chunked & 7) == 0 && p.row_stride <= far / 256 &&
+                      p.other_stride <= far / 256 &&
+                      (!all_x || p.row_stride <= far / (p.x_rows + 1));
   if (type == kGmmMX4) {
     const uintptr_t scales = reinterpret_cast<uintptr_t>(p.row_scales) |
                              reinterpret_cast<uintptr_t>(p.other_scales) | uintptr_t(p.blocks);
