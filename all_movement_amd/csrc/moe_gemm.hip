@@ -265,6 +265,16 @@ __device__ inline int4v load_part(const uint8_t* p, int n) {
   return r;
 }
 
+// The last n (1..7) elements of 8, moved to the front, with zeros after them.
+__device__ inline int4v last_part(int4v v, int n) {
+  const uint64_t lo = uint32_t(v[0]) | uint64_t(uint32_t(v[1])) << 32;
+  const uint64_t hi = uint32_t(v[2]) | uint64_t(uint32_t(v[3])) << 32;
+  const int drop = 16 * (8 - n);  // bits, 16..112
+  const uint64_t a = drop < 64 ? lo >> drop | hi << (64 - drop) : hi >> (drop - 64);
+  const uint64_t b = drop < 64 ? hi >> drop : 0;
+  return int4v{int(uint32_t(a)), int(a >> 32), int(uint32_t(b)), int(b >> 32)};
+}
+
 // The same through LDS (free by now, a part of it per wave): the fragments'
 // pieces of 8 or 16 bytes become rows, which leave in whole lines.  Straight
 // from the fragments every line of the output was written in four parts, and a
@@ -453,9 +463,27 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
 
   const uint32_t lds0 = uint32_t(uintptr_t((lds_u8*)lds));
 
+  // Not DIRECT: the chunk that a row ends in is loaded as the row's last 8
+  // elements and moved into place on its way to LDS, so that no step waits for
+  // it where it is loaded (1539 rows of 7 experts, 1001 x 523: dx 28 us when its
+  // elements were joined there, 19 so).  Only rows shorter than 8 are loaded by
+  // element.
+  const bool short_rows = (kRowsAlong ? red : p.N) < 8;
+  const bool short_cols = (kColsAlong ? red : p.K) < 8;
+  if constexpr (!DIRECT) {
+    // Across, it is the same chunk in every step.
+#pragma unroll
+    for (int i = 0; i < q.kPer; ++i)
+      if (!kRowsAlong && !short_rows && q.left[i] > 0 && q.left[i] < 8)
+        q.ptr[i] -= 2 * (8 - q.left[i]);
+#pragma unroll
+    for (int i = 0; i < c.kPer; ++i)
+      if (!kColsAlong && !short_cols && c.left[i] > 0 && c.left[i] < 8)
+        c.ptr[i] -= 2 * (8 - c.left[i]);
+  }
   // Loads step k into buffer k & 1 (or, not DIRECT, into registers).
-  auto load_one = [&](auto& ld, auto along, int i, int k, auto odd, uint32_t base,
-                      const uint8_t* ptr) {
+  auto load_one = [&](auto& ld, auto along, bool short_line, int i, int k, auto odd,
+                      uint32_t base, const uint8_t* ptr) {
     constexpr bool kAlong = decltype(along)::value;
     int n;  // elements of the chunk that exist
     if (kAlong) {
@@ -468,7 +496,13 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       load_to_lds(n > 0 ? ptr : zeros,
                   __builtin_amdgcn_readfirstlane(base + (wave * ld.kPer + i) * 1024));
     } else {
-      ld.staged[decltype(odd)::value][i] = n > 0 ? load_part(ptr, n) : int4v{0, 0, 0, 0};
+      int4v v = {0, 0, 0, 0};
+      if (short_line) {
+        if (n > 0) v = load_part(ptr, n);
+      } else if (n > 0) {
+        v = load_part(kAlong && n < 8 ? ptr - 2 * (8 - n) : ptr, 8);
+      }
+      ld.staged[decltype(odd)::value][i] = v;
     }
   };
   // dw: the rows of x of the next step to issue, read a step ahead so that
@@ -509,7 +543,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
     for (int i = 0; i < q.kPer; ++i) {
       const uint8_t* ptr = q.ptr[i];
       if (ptr) ptr += kRowsAlong ? int64_t(k) * 128 : int64_t(k) * 64 * p.row_stride;
-      load_one(q, row_kind, i, k, odd, base, ptr);
+      load_one(q, row_kind, short_rows, i, k, odd, base, ptr);
     }
 #pragma unroll
     for (int i = 0; i < c.kPer; ++i) {
@@ -522,19 +556,27 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
         const int row = next_row[i];
         ptr = row < 0 ? nullptr : ptr + int64_t(row) * p.other_stride;
       }
-      load_one(c, col_kind, i, k, odd, base + BM * 128, ptr);
+      load_one(c, col_kind, short_cols, i, k, odd, base + BM * 128, ptr);
     }
   };
-  auto put_staged = [&](auto odd) {
+  auto put_staged = [&](int k, auto odd) {
     if constexpr (!DIRECT) {
       constexpr int kOdd = decltype(odd)::value;
       uint8_t* b = lds + kOdd * kBuf;
+      auto placed = [&](const auto& ld, auto along, bool short_line, int i) {
+        int4v v = ld.staged[kOdd][i];
+        const int n = ld.left[i] - (decltype(along)::value ? k * kStep : 0);
+        if (n > 0 && n < 8 && !short_line) v = last_part(v, n);
+        return v;
+      };
 #pragma unroll
       for (int i = 0; i < q.kPer; ++i)
-        *reinterpret_cast<int4v*>(b + q.chunk(i) * 16) = q.staged[kOdd][i];
+        *reinterpret_cast<int4v*>(b + q.chunk(i) * 16) =
+            placed(q, std::integral_constant<bool, kRowsAlong>{}, short_rows, i);
 #pragma unroll
       for (int i = 0; i < c.kPer; ++i)
-        *reinterpret_cast<int4v*>(b + BM * 128 + c.chunk(i) * 16) = c.staged[kOdd][i];
+        *reinterpret_cast<int4v*>(b + BM * 128 + c.chunk(i) * 16) =
+            placed(c, std::integral_constant<bool, kColsAlong>{}, short_cols, i);
     }
   };
 
@@ -642,7 +684,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       issue(1, kOdd);
       read_rows(2);
     }
-    put_staged(kEven);
+    put_staged(0, kEven);
   }
   auto step = [&](int k, auto odd) {
     constexpr auto other = std::integral_constant<int, decltype(odd)::value ^ 1>{};
@@ -658,7 +700,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       read_rows(k + kAhead + 1);
     }
     compute(k);
-    if (k + 1 < steps) put_staged(other);
+    if (k + 1 < steps) put_staged(k + 1, other);
   };
   int k = 0;
   for (; k + 1 < steps; k += 2) {

@@ -234,6 +234,26 @@ def test_every_product_is_in_the_sums_that_are_stored(dt):
         check_all(gen, counts, N, K, dt)
 
 
+@pytest.mark.parametrize("N,K", [(64 + t, 200 - t) for t in range(1, 8)]
+                         + [(8 + t, 8 - t) for t in range(1, 8)]
+                         + [(8 - t, 8 + t) for t in range(1, 8)] + [(7, 5), (129, 521)])
+def test_row_ends_of_every_length(N, K):
+    """Rows that end inside a piece of 8 elements, with NaN before and after them."""
+    gen = torch.Generator().manual_seed(N * 1000 + K)
+    x, w, dy, c = make(gen, 160, 3, N, K, torch.bfloat16, [90, 0, 70])
+
+    def among_nan(t, pad):
+        flat = torch.full((t[..., 0].numel() * (t.shape[-1] + pad) + 22,), float("nan"),
+                          dtype=t.dtype, device=DEV)[11:-11]
+        v = flat.view(*t.shape[:-1], t.shape[-1] + pad)[..., :t.shape[-1]]
+        return v.copy_(t)
+    xn, wn, dyn = among_nan(x, 5), among_nan(w, 0), among_nan(dy, 9)
+    print("N", N, "K", K, flush=True)
+    plain.check_sums(moe.gmm(xn, wn, c, check=True), *plain.gmm(x, w, c), K)
+    plain.check_sums(moe.gmm_dx(dyn, wn, c, check=True), *plain.gmm_dx(dy, w, c), N)
+    plain.check_sums(moe.gmm_dw(dyn, xn, c, check=True), *plain.gmm_dw(dy, x, c), 90)
+
+
 def test_far_rows_take_the_plain_loads():
     """A stride of which 256 rows pass 4 GiB: the same values as close together."""
     gen = torch.Generator().manual_seed(8)
