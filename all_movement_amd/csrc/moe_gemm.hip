@@ -209,13 +209,19 @@ __device__ inline uint16_t round16(float v, int type) {
   return __builtin_bit_cast(uint16_t, _Float16(v));
 }
 
-// A lane holds 4 columns (4g .. 4g + 3 of a fragment) of output row l16.
+// A lane holds 4 columns (4g .. 4g + 3 of a fragment) of output row l16, stored
+// at once at any alignment of an element.
 template <int MODE, int TM, int TN, int FM, int FN>
 __device__ inline void store_tile(const GmmParams& p, const Tile& t, const float4v (&acc)[FM][FN],
                                   int wm, int wn) {
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int64_t first = MODE == kGmmDw ? int64_t(t.span.e) * p.N + t.out_row0 : t.out_row0;
-  const bool wide = (p.out_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  struct __attribute__((packed, aligned(4))) Loose32 {
+    float4v v;
+  };
+  struct __attribute__((packed, aligned(2))) Loose16 {
+    uint64_t v;
+  };
 #pragma unroll
   for (int a = 0; a < FM; ++a) {
     const int r = wm * TM + a * 16 + l16;
@@ -226,11 +232,11 @@ __device__ inline void store_tile(const GmmParams& p, const Tile& t, const float
       if (col >= t.cn) continue;
       const int64_t at = (first + r) * p.out_stride + t.c0 + col;
       const float4v v = acc[a][d];
-      const bool whole = wide && col + 4 <= t.cn;
+      const bool whole = col + 4 <= t.cn;
       if (p.out_type == A2AV_FP32) {
         float* o = reinterpret_cast<float*>(p.out) + at;
         if (whole)
-          *reinterpret_cast<float4v*>(o) = v;
+          reinterpret_cast<Loose32*>(o)->v = v;
         else
           for (int i = 0; i < 4 && col + i < t.cn; ++i) o[i] = v[i];
       } else {
@@ -239,7 +245,7 @@ __device__ inline void store_tile(const GmmParams& p, const Tile& t, const float
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = round16(v[i], p.out_type);
         if (whole)
-          *reinterpret_cast<uint64_t*>(o) = __builtin_bit_cast(uint64_t, h);
+          reinterpret_cast<Loose16*>(o)->v = __builtin_bit_cast(uint64_t, h);
         else
           for (int i = 0; i < 4 && col + i < t.cn; ++i) o[i] = h[i];
       }
