@@ -73,7 +73,8 @@ int a2av_moe_route(const void *logits, int64_t logits_stride, int64_t tokens, in
 
 /* The gradient of the weights with respect to the logits:
  *   dlogits[t][e] = q_e * (g_e - sum_j weights[t][j] * dweights[t][j])
- * with g_e = dweights of the slot that chose e (0 if none) and q = softmax of
+ * with g_e = dweights of the slot that chose e (0 if none; a token's slots
+ * choose different experts, as the router's do) and q = softmax of
  * the logits, or with renormalize != 0 the weights themselves (0 where not
  * chosen).  Empty slots' dweights are not read into the sum; logits of -inf
  * get 0.  dlogits [tokens, E] has the logits' dtype and is contiguous.  An

@@ -117,6 +117,28 @@ def test_gradient(dt, renorm, T, E, k):
 
 
 @pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k", [(64, 3), (250, 8), (700, 16)])
+def test_gradient_of_many_tokens(renorm, E, k):
+    """More tokens than waves: nothing of a token is left for the next; some
+    tokens have empty slots, some no expert at all."""
+    gen = torch.Generator().manual_seed(E + k)
+    T = 20011
+    l = torch.randn(T, E, generator=gen) * 2
+    l[::7] = -float("inf")
+    l[3::11, 2:] = -float("inf")
+    l = l.to(DEV)
+    r = moe.route(l, k, renormalize=renorm)
+    dw = torch.randn(T, k, generator=gen).to(DEV)
+    dw[r.experts < 0] = float("nan")
+    got = moe.route_backward(l, r.experts, r.weights, dw, renormalize=renorm).double().cpu().numpy()
+    want = plain.route_back(l.cpu().numpy(), r.experts.cpu().numpy(), r.weights.cpu().numpy(),
+                            dw.cpu().numpy(), renorm)
+    size = np.abs(np.nan_to_num(dw.cpu().numpy())).max()
+    tol = (weight_tol(E) + (k + 4) * 2.0 ** -23) * size * 3 + plain.step(torch.float32) * np.abs(want)
+    assert np.all(np.abs(got - want) <= tol + torch.finfo(torch.float32).smallest_normal)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
 def test_gradient_against_differences(renorm):
     gen = torch.Generator().manual_seed(12)
     l = torch.randn(3, 10, generator=gen)
