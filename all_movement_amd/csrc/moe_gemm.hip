@@ -15,6 +15,7 @@
 
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 #include "a2av.h"
 #include "moe.h"
@@ -258,7 +259,10 @@ __device__ inline int4v load_part(const uint8_t* p, int n) {
   struct __attribute__((packed, aligned(2))) Loose {
     int4v v;
   };
-  if (n >= 8) return reinterpret_cast<const Loose*>(p)->v;
+  // As global memory: where the compiler cannot see that, it counts the load
+  // as one of LDS too, and any wait is then for all of them.
+  if (n >= 8)
+    return reinterpret_cast<const __attribute__((address_space(1))) Loose*>(uintptr_t(p))->v;
   int4v r = {0, 0, 0, 0};
   const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
@@ -344,20 +348,27 @@ __device__ inline int across_swizzle(int r) {
   return (2 * (r & 3) | (8 & r)) & (SPAN / 8 - 1);
 }
 
+// f(0), f(1), .., each number as a type.
+template <int... I, class F>
+__device__ inline void each(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+
 // One operand's tile of SPAN outputs x 128 bytes of reduction, loaded by NW
 // waves as 16-byte chunks.
 //   along:  LDS [SPAN][8 chunks], chunk c of row r at c ^ (r & 7)
 //   across: LDS [64][SPAN / 8 chunks], chunk c of row r at c ^ f(r),
 //           f(r) = 2 (r & 3) + 8 (r >> 3 & 1)
 // so that the reads of one fragment spread over all LDS banks.
-template <bool ALONG, int SPAN, int NW, bool DIRECT>
+// AHEAD: the steps on their way in registers; 0: loads go straight to LDS.
+template <bool ALONG, int SPAN, int NW, int AHEAD>
 struct Loader {
   static constexpr int kChunks = SPAN * 8;
   static constexpr int kPer = kChunks / (NW * 64);  // chunks per lane
   static_assert(kChunks % (NW * 64) == 0, "a tile is a whole number of wave loads");
   const uint8_t* ptr[kPer];
   int32_t left[kPer];   // along: elements of the row from this chunk on; across: columns from it
-  int4v staged[2][DIRECT ? 1 : kPer];  // steps of even and odd number
+  int4v staged[AHEAD ? AHEAD : 1][AHEAD ? kPer : 1];  // by the step's number % AHEAD
   int wave, lane;
 
   __device__ int chunk(int i) const { return (wave * kPer + i) * 64 + lane; }
@@ -399,7 +410,7 @@ __device__ inline float4v mma_mx4(int4v a, int4v b, float4v c, int sa, int sb, i
 }
 
 // BM rows x BN columns of the output by WM x WN waves.
-template <int TY, int MODE, int BM, int BN, int WM, int WN, bool DIRECT>
+template <int TY, int MODE, int BM, int BN, int WM, int WN, bool DIRECT, bool SHORT = false>
 __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
   constexpr int NW = WM * WN;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
@@ -407,6 +418,11 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
   constexpr bool kRowsAlong = MODE != kGmmDw;   // the operand of the output's rows
   constexpr int kStep = TY == kGmmMX4 ? 256 : 64;  // reduction elements per step
   constexpr int kPerChunk = kStep / 8;
+  // Loads run kAhead steps ahead: straight to LDS into the other buffer, or by
+  // way of registers, which the step before puts into LDS.  Four steps ahead were
+  // no faster (dx 14.3 us for 13.8 at the sizes below) and cost waves.
+  constexpr int kAhead = DIRECT ? 1 : 2;
+  constexpr bool kSkip = MODE == kGmmDw && BM == 64;  // no loads of rows that are not there
   constexpr int kBuf = (BM + BN) * 128;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBuf];
 
@@ -425,8 +441,8 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
   const int steps = int((red + kStep - 1) / kStep);
 
   // ---- the loaders: where each chunk of a lane begins, without the step.
-  Loader<kRowsAlong, BM, NW, DIRECT> q;
-  Loader<kColsAlong, BN, NW, DIRECT> c;
+  Loader<kRowsAlong, BM, NW, DIRECT ? 0 : kAhead> q;
+  Loader<kColsAlong, BN, NW, DIRECT ? 0 : kAhead> c;
   q.wave = c.wave = wave;
   q.lane = c.lane = lane;
   const uint8_t* zeros = reinterpret_cast<const uint8_t*>(g_zeros);
@@ -472,24 +488,22 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
   // Not DIRECT: the chunk that a row ends in is loaded as the row's last 8
   // elements and moved into place on its way to LDS, so that no step waits for
   // it where it is loaded (1539 rows of 7 experts, 1001 x 523: dx 28 us when its
-  // elements were joined there, 19 so).  Only rows shorter than 8 are loaded by
-  // element.
-  const bool short_rows = (kRowsAlong ? red : p.N) < 8;
-  const bool short_cols = (kColsAlong ? red : p.K) < 8;
-  if constexpr (!DIRECT) {
+  // elements were joined there, 19 so).  Rows shorter than 8 (SHORT) are
+  // loaded by element.
+  if constexpr (!DIRECT && !SHORT) {
     // Across, it is the same chunk in every step.
 #pragma unroll
     for (int i = 0; i < q.kPer; ++i)
-      if (!kRowsAlong && !short_rows && q.left[i] > 0 && q.left[i] < 8)
+      if (!kRowsAlong && q.left[i] > 0 && q.left[i] < 8)
         q.ptr[i] -= 2 * (8 - q.left[i]);
 #pragma unroll
     for (int i = 0; i < c.kPer; ++i)
-      if (!kColsAlong && !short_cols && c.left[i] > 0 && c.left[i] < 8)
+      if (!kColsAlong && c.left[i] > 0 && c.left[i] < 8)
         c.ptr[i] -= 2 * (8 - c.left[i]);
   }
   // Loads step k into buffer k & 1 (or, not DIRECT, into registers).
-  auto load_one = [&](auto& ld, auto along, bool short_line, int i, int k, auto odd,
-                      uint32_t base, const uint8_t* ptr) {
+  auto load_one = [&](auto& ld, auto along, int i, int k, auto set, uint32_t base,
+                      const uint8_t* ptr) {
     constexpr bool kAlong = decltype(along)::value;
     int n;  // elements of the chunk that exist
     if (kAlong) {
@@ -502,13 +516,20 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       load_to_lds(n > 0 ? ptr : zeros,
                   __builtin_amdgcn_readfirstlane(base + (wave * ld.kPer + i) * 1024));
     } else {
+      // Without a branch: across one, the compiler waits for all loads at once
+      // (1539 rows of 7 experts, 1001 x 523: dx 18.1 -> 13.6 us, with the loop
+      // below).  dw's small tiles have reductions of few steps, and rows that
+      // are not there are better skipped (15.8 -> 12.7; large ones 44.5 -> 48).
       int4v v = {0, 0, 0, 0};
-      if (short_line) {
+      if constexpr (SHORT) {
         if (n > 0) v = load_part(ptr, n);
-      } else if (n > 0) {
-        v = load_part(kAlong && n < 8 ? ptr - 2 * (8 - n) : ptr, 8);
+      } else if constexpr (kSkip) {
+        if (n > 0) v = load_part(ptr, 8);
+      } else {
+        if (kAlong && n < 8) ptr -= 2 * (8 - n);
+        v = load_part(n > 0 ? ptr : zeros, 8);
       }
-      ld.staged[decltype(odd)::value][i] = v;
+      ld.staged[decltype(set)::value][i] = v;
     }
   };
   // dw: the rows of x of the next step to issue, read a step ahead so that
@@ -540,7 +561,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       }
     }
   };
-  auto issue = [&](int k, auto odd) {
+  auto issue = [&](int k, auto set) {
     check_rows(k);
     const uint32_t base = lds0 + (k & 1) * kBuf;
     constexpr auto row_kind = std::integral_constant<bool, kRowsAlong>{};
@@ -549,7 +570,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
     for (int i = 0; i < q.kPer; ++i) {
       const uint8_t* ptr = q.ptr[i];
       if (ptr) ptr += kRowsAlong ? int64_t(k) * 128 : int64_t(k) * 64 * p.row_stride;
-      load_one(q, row_kind, short_rows, i, k, odd, base, ptr);
+      load_one(q, row_kind, i, k, set, base, ptr);
     }
 #pragma unroll
     for (int i = 0; i < c.kPer; ++i) {
@@ -562,27 +583,27 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
         const int row = next_row[i];
         ptr = row < 0 ? nullptr : ptr + int64_t(row) * p.other_stride;
       }
-      load_one(c, col_kind, short_cols, i, k, odd, base + BM * 128, ptr);
+      load_one(c, col_kind, i, k, set, base + BM * 128, ptr);
     }
   };
-  auto put_staged = [&](int k, auto odd) {
+  auto put_staged = [&](int k, auto set) {
     if constexpr (!DIRECT) {
-      constexpr int kOdd = decltype(odd)::value;
-      uint8_t* b = lds + kOdd * kBuf;
-      auto placed = [&](const auto& ld, auto along, bool short_line, int i) {
-        int4v v = ld.staged[kOdd][i];
+      constexpr int kSet = decltype(set)::value;
+      uint8_t* b = lds + (kSet & 1) * kBuf;
+      auto placed = [&](const auto& ld, auto along, int i) {
+        int4v v = ld.staged[kSet][i];
         const int n = ld.left[i] - (decltype(along)::value ? k * kStep : 0);
-        if (n > 0 && n < 8 && !short_line) v = last_part(v, n);
+        if (!SHORT && n > 0 && n < 8) v = last_part(v, n);
         return v;
       };
 #pragma unroll
       for (int i = 0; i < q.kPer; ++i)
         *reinterpret_cast<int4v*>(b + q.chunk(i) * 16) =
-            placed(q, std::integral_constant<bool, kRowsAlong>{}, short_rows, i);
+            placed(q, std::integral_constant<bool, kRowsAlong>{}, i);
 #pragma unroll
       for (int i = 0; i < c.kPer; ++i)
         *reinterpret_cast<int4v*>(b + BM * 128 + c.chunk(i) * 16) =
-            placed(c, std::integral_constant<bool, kColsAlong>{}, short_cols, i);
+            placed(c, std::integral_constant<bool, kColsAlong>{}, i);
     }
   };
 
@@ -677,23 +698,20 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
     end_of_products();
   };
 
-  // Loads run kAhead steps ahead: straight to LDS into the other buffer, or by
-  // way of registers, which the step before puts into LDS.
-  constexpr int kAhead = DIRECT ? 1 : 2;
-  constexpr auto kEven = std::integral_constant<int, 0>{};
-  constexpr auto kOdd = std::integral_constant<int, 1>{};
+  using Sets = std::make_integer_sequence<int, kAhead>;
   if (steps > 0) {
     read_rows(0);
-    issue(0, kEven);
-    read_rows(1);
-    if (!DIRECT && steps > 1) {
-      issue(1, kOdd);
-      read_rows(2);
-    }
-    put_staged(0, kEven);
+    each(Sets{}, [&](auto set) {
+      constexpr int k = decltype(set)::value;
+      if (k < steps) {
+        issue(k, set);
+        read_rows(k + 1);
+      }
+    });
+    put_staged(0, std::integral_constant<int, 0>{});
   }
-  auto step = [&](int k, auto odd) {
-    constexpr auto other = std::integral_constant<int, decltype(odd)::value ^ 1>{};
+  // k % kAhead is `set`; `inner`: kAhead more steps follow.
+  auto step = [&](int k, auto set, auto inner) {
     if constexpr (DIRECT) {
       wait_loads_and_barrier();
     } else {
@@ -701,19 +719,24 @@ __global__ __launch_bounds__(WM* WN * 64) void gmm_kernel(const GmmParams p) {
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     }
-    if (k + kAhead < steps) {
-      issue(k + kAhead, odd);
+    if (decltype(inner)::value || k + kAhead < steps) {
+      issue(k + kAhead, set);
       read_rows(k + kAhead + 1);
     }
     compute(k);
-    if (k + 1 < steps) put_staged(k + 1, other);
+    if (decltype(inner)::value || k + 1 < steps)
+      put_staged(k + 1, std::integral_constant<int, (decltype(set)::value + 1) % kAhead>{});
   };
+  // Without conditions a wait for a step's loads leaves those of later ones on
+  // their way.
   int k = 0;
-  for (; k + 1 < steps; k += 2) {
-    step(k, kEven);
-    step(k + 1, kOdd);
-  }
-  if (k < steps) step(k, kEven);
+  for (; !kSkip && k + 2 * kAhead <= steps; k += kAhead)
+    each(Sets{}, [&](auto set) { step(k + decltype(set)::value, set, std::true_type{}); });
+  for (; k < steps; k += kAhead)
+    each(Sets{}, [&](auto set) {
+      if (k + decltype(set)::value < steps)
+        step(k + decltype(set)::value, set, std::false_type{});
+    });
   if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
 
   store_tile<MODE, TM, TN, FM, FN>(p, t, acc, wm, wn);
@@ -1417,6 +1440,9 @@ hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
     return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 4>, 256, p, stream);
   }
   if constexpr (TY != kGmmMX4) {
+    if (p.K < 8 || (MODE != kGmmFwd && p.N < 8))  // rows of an operand
+      return launch_tiles<MODE, 64, 64>(gmm_kernel<TY, MODE, 64, 64, 2, 2, false, true>, 256, p,
+                                        stream);
     const int64_t used = p.E < p.nrows ? p.E : p.nrows;
     const int64_t cols = ((MODE == kGmmFwd ? p.N : p.K) + 127) / 128;
     const int64_t rows = MODE == kGmmDw ? int64_t(p.E) * ((p.N + 127) / 128)
