@@ -29,6 +29,7 @@ struct Operand {
   bool out;
   int64_t align;  // bytes the address has to be a multiple of
   bool optional = false;
+  int64_t stride = 0, width = 0;  // bytes of strided rows; 0: all of it is one run
 };
 
 // Bytes from a matrix's first row to the end of its last.
@@ -39,11 +40,73 @@ int64_t extent(int64_t rows, int64_t stride, int64_t width, int64_t size) {
   return n < (int64_t(1) << 58) ? n * size : int64_t(1) << 60;
 }
 
+// A matrix's rows; of bad sizes, something that must not be NULL.
+Operand matrix(const void* p, bool bad, int64_t rows, int64_t stride, int64_t width, int64_t size,
+               bool out, bool optional = false) {
+  if (bad) return Operand{p, 1, out, size, optional};
+  return Operand{p, extent(rows, stride, width, size), out, size, optional, stride * size,
+                 width * size};
+}
+
 // NULLPTR, then nothing else; the addresses' other checks come last.
 bool any_null(std::initializer_list<Operand> all) {
   for (const Operand& o : all)
     if (!o.p && !o.optional && o.bytes > 0) return true;
   return false;
+}
+
+// sum over i < n of floor((a i + b) / m), modulo 2^64, by the steps of Euclid's
+// algorithm on a and m.
+uint64_t sum_of_floors(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
+  uint64_t sum = 0;
+  for (;;) {
+    sum += (n & 1 ? n * ((n - 1) / 2) : n / 2 * (n - 1)) * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const uint64_t top = a * n + b;
+    if (top < m) return sum;
+    n = top / m;
+    b = top % m;
+    const uint64_t t = m;
+    m = a;
+    a = t;
+  }
+}
+
+// Whether two operands share a byte: rows of one may lie between the other's
+// (columns of one buffer).
+bool share_bytes(const Operand& one, const Operand& two) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(one.p), y = reinterpret_cast<uintptr_t>(two.p);
+  if (!(x < y + uintptr_t(two.bytes) && y < x + uintptr_t(one.bytes))) return false;
+  const bool swap = two.stride == two.width;
+  const Operand& a = swap ? two : one;
+  const Operand& b = swap ? one : two;
+  // Larger than any address space (cut by extent): the rows are not told apart.
+  if (b.stride == b.width || a.bytes >= int64_t(1) << 60 || b.bytes >= int64_t(1) << 60)
+    return true;
+  // at + i step, `len` bytes: the rows of a, from the start of b on.
+  int64_t at = reinterpret_cast<intptr_t>(a.p) - reinterpret_cast<intptr_t>(b.p);
+  const bool rows = a.stride > a.width;
+  const int64_t len = rows ? a.width : a.bytes, step = rows ? a.stride : 1;
+  int64_t n = rows ? (a.bytes - len) / step + 1 : 1;
+  if (at + len <= 0) {  // rows before b
+    const int64_t before = -(at + len) / step + 1;
+    if (before >= n) return false;
+    n -= before;
+    at += before * step;
+  }
+  if (at >= b.bytes) return false;
+  if (at <= 0) return true;
+  const int64_t inside = (b.bytes - at + step - 1) / step;
+  if (inside < n) n = inside;
+  // Each of these begins before b's end, so it shares a byte with a row of b
+  // exactly if its place in b's stride is less than b.width, or less than `len`
+  // before the next row: if (at + len - 1) mod b.stride < b.width + len - 1.
+  const int64_t hit = b.width + len - 1;
+  if (hit >= b.stride) return true;
+  const uint64_t m = uint64_t(b.stride), from = uint64_t(at + len - 1) % m, a1 = uint64_t(step) % m;
+  return sum_of_floors(uint64_t(n), m, a1, from + m) !=
+         sum_of_floors(uint64_t(n), m, a1, from + m - uint64_t(hit));
 }
 
 // Misaligned, or an output that shares a byte with another operand.
@@ -53,8 +116,7 @@ bool bad_addresses(std::initializer_list<Operand> all) {
   for (const Operand* a = all.begin(); a != all.end(); ++a)
     for (const Operand* b = a + 1; b != all.end(); ++b) {
       if (!(a->out || b->out) || !a->p || !b->p || a->bytes <= 0 || b->bytes <= 0) continue;
-      const uintptr_t x = reinterpret_cast<uintptr_t>(a->p), y = reinterpret_cast<uintptr_t>(b->p);
-      if (x < y + uintptr_t(b->bytes) && y < x + uintptr_t(a->bytes)) return true;
+      if (share_bytes(*a, *b)) return true;
     }
   return false;
 }
@@ -96,19 +158,17 @@ int a2av_moe_route(const void* logits, int64_t logits_stride, int64_t tokens, in
   const int64_t slots = tokens > 0 && k > 0 && tokens <= kMax31 && k <= kMax31 ? tokens * k : 0;
   int64_t need = 0;
   const int sizes = a2av_moe_route_workspace(tokens, E, k, &need);
+  const bool bad = sizes != A2AV_OK || logits_stride < E || logits_stride > kMax31;
   const int64_t z = size_of(dtype);
   const std::initializer_list<Operand> all = {
-      {logits, sizes ? slots : extent(tokens, logits_stride, E, z), false, z},
+      matrix(logits, bad && slots > 0, bad ? 0 : tokens, logits_stride, E, z, false),
       {experts, slots * 4, true, 4},   {weights, slots * 4, true, 4},
       {counts, int64_t(E > 0 ? E : 0) * 4, true, 4},
       {order, slots * 4, true, 4},     {place, slots * 4, true, 4},
       {workspace, need, true, 16}};
   if (any_null(all)) return A2AV_ERR_NULLPTR;
   if (!is_float(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
-  if (sizes != A2AV_OK) return sizes;
-  if (logits_stride < E || logits_stride > kMax31 || workspace_bytes < need ||
-      bad_addresses(all))
-    return A2AV_ERR_INVALID_ARGS;
+  if (bad || workspace_bytes < need || bad_addresses(all)) return A2AV_ERR_INVALID_ARGS;
   RouteParams p{};
   p.logits = logits;
   p.stride = logits_stride;
@@ -132,18 +192,17 @@ int a2av_moe_route_backward(const void* logits, int64_t logits_stride, int64_t t
                             void* stream) {
   const int sizes = check_route_sizes(tokens, E, k);
   const int64_t slots = sizes ? (tokens > 0) : tokens * k;
+  const bool bad = sizes != A2AV_OK || logits_stride < E || logits_stride > kMax31;
   const int64_t z = size_of(dtype);
   const std::initializer_list<Operand> all = {
-      {logits, sizes ? slots : extent(tokens, logits_stride, E, z), false, z},
+      matrix(logits, bad && slots > 0, bad ? 0 : tokens, logits_stride, E, z, false),
       {experts, slots * 4, false, 4},
       {weights, slots * 4, false, 4},
       {dweights, slots * 4, false, 4},
       {dlogits, sizes ? slots : tokens * E * z, true, z}};
   if (any_null(all)) return A2AV_ERR_NULLPTR;
   if (!is_float(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
-  if (sizes != A2AV_OK) return sizes;
-  if (logits_stride < E || logits_stride > kMax31 || bad_addresses(all))
-    return A2AV_ERR_INVALID_ARGS;
+  if (bad || bad_addresses(all)) return A2AV_ERR_INVALID_ARGS;
   RouteBackParams p{};
   p.logits = logits;
   p.stride = logits_stride;
@@ -167,11 +226,11 @@ int a2av_moe_gmm(const void* x, int64_t x_stride, int64_t x_rows, const void* w,
                          x_stride > kMax31 || y_stride < N || y_stride > kMax31;
   const bool some = sizes_bad || rows > 0;
   const std::initializer_list<Operand> all = {
-      {x, sizes_bad ? 1 : extent(x_rows, x_stride, K, 2), false, 2},
+      matrix(x, sizes_bad, x_rows, x_stride, K, 2, false),
       {w, sizes_bad ? 1 : E * N * K * 2, false, 2},
       {counts, sizes_bad ? 1 : int64_t(E) * 4, false, 4},
       {index, sizes_bad ? 1 : rows * 4, false, 4, true},
-      {y, sizes_bad ? 1 : extent(rows, y_stride, N, 2), true, 2},
+      matrix(y, sizes_bad, rows, y_stride, N, 2, true),
       {status, 4, true, 4, true}};
   if (some && any_null(all)) return A2AV_ERR_NULLPTR;
   if (!is_16bit(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
@@ -204,10 +263,10 @@ int a2av_moe_gmm_dx(const void* dy, int64_t dy_stride, const void* w, const int3
                          dy_stride > kMax31 || dx_stride < K || dx_stride > kMax31;
   const bool some = sizes_bad || rows > 0;
   const std::initializer_list<Operand> all = {
-      {dy, sizes_bad ? 1 : extent(rows, dy_stride, N, 2), false, 2},
+      matrix(dy, sizes_bad, rows, dy_stride, N, 2, false),
       {w, sizes_bad ? 1 : E * N * K * 2, false, 2},
       {counts, sizes_bad ? 1 : int64_t(E) * 4, false, 4},
-      {dx, sizes_bad ? 1 : extent(rows, dx_stride, K, 2), true, 2},
+      matrix(dx, sizes_bad, rows, dx_stride, K, 2, true),
       {status, 4, true, 4, true}};
   if (some && any_null(all)) return A2AV_ERR_NULLPTR;
   if (!is_16bit(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
@@ -240,8 +299,8 @@ int a2av_moe_gmm_dw(const void* dy, int64_t dy_stride, const void* x, int64_t x_
                          dy_stride > kMax31 || x_stride < K || x_stride > kMax31;
   const int64_t dz = size_of(dw_dtype);
   const std::initializer_list<Operand> all = {
-      {dy, sizes_bad ? 1 : extent(rows, dy_stride, N, 2), false, 2},
-      {x, sizes_bad ? 1 : extent(rows ? x_rows : 0, x_stride, K, 2), false, 2},
+      matrix(dy, sizes_bad, rows, dy_stride, N, 2, false),
+      matrix(x, sizes_bad, rows ? x_rows : 0, x_stride, K, 2, false),
       {counts, sizes_bad ? 1 : int64_t(E) * 4, false, 4},
       {index, sizes_bad ? 1 : rows * 4, false, 4, true},
       {dw, sizes_bad ? 1 : E * N * K * dz, true, dz},
@@ -278,10 +337,10 @@ int a2av_moe_combine(const void* y, int64_t y_stride, int64_t y_rows, const int3
                          out_stride < width || out_stride > kMax31;
   const int64_t z = size_of(dtype);
   const std::initializer_list<Operand> all = {
-      {y, sizes_bad ? 1 : extent(tokens ? y_rows : 0, y_stride, width, z), false, z},
+      matrix(y, sizes_bad, tokens ? y_rows : 0, y_stride, width, z, false),
       {place, sizes_bad ? 1 : tokens * k * 4, false, 4},
       {weights, sizes_bad ? 1 : tokens * k * 4, false, 4, true},
-      {out, sizes_bad ? 1 : extent(tokens, out_stride, width, z), true, z},
+      matrix(out, sizes_bad, tokens, out_stride, width, z, true),
       {status, 4, true, 4, true}};
   if (any_null(all)) return A2AV_ERR_NULLPTR;
   if (!is_float(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
@@ -314,13 +373,12 @@ int a2av_moe_combine_backward(const void* dout, int64_t dout_stride, const void*
                          dy_stride > kMax31;
   const int64_t z = size_of(dtype);
   const std::initializer_list<Operand> all = {
-      {dout, sizes_bad ? 1 : extent(tokens, dout_stride, width, z), false, z},
+      matrix(dout, sizes_bad, tokens, dout_stride, width, z, false),
       // y is only read for dweights
-      {y, sizes_bad ? 1 : extent(tokens ? y_rows : 0, y_stride, width, z), false, z,
-       dweights == nullptr},
+      matrix(y, sizes_bad, tokens ? y_rows : 0, y_stride, width, z, false, dweights == nullptr),
       {place, sizes_bad ? 1 : tokens * k * 4, false, 4},
       {weights, sizes_bad ? 1 : tokens * k * 4, false, 4, true},
-      {dy, sizes_bad ? 1 : extent(tokens ? y_rows : 0, dy_stride, width, z), true, z},
+      matrix(dy, sizes_bad, tokens ? y_rows : 0, dy_stride, width, z, true),
       {dweights, sizes_bad ? 1 : tokens * k * 4, true, 4, weights == nullptr},
       {status, 4, true, 4, true}};
   if (any_null(all)) return A2AV_ERR_NULLPTR;
@@ -352,7 +410,7 @@ int a2av_moe_mx4_quantize(const void* x, int64_t x_stride, int64_t rows, int64_t
                          x_stride > kMax31;
   const int64_t z = size_of(dtype), blocks = (cols + 31) / 32;
   const std::initializer_list<Operand> all = {
-      {x, sizes_bad ? 1 : extent(rows, x_stride, cols, z), false, z},
+      matrix(x, sizes_bad, rows, x_stride, cols, z, false),
       {codes, sizes_bad ? 1 : rows * blocks * 16, true, 16},
       {scales, sizes_bad ? 1 : rows * blocks, true, 1}};
   if (any_null(all)) return A2AV_ERR_NULLPTR;
@@ -379,7 +437,7 @@ int a2av_moe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t
   const std::initializer_list<Operand> all = {
       {codes, sizes_bad ? 1 : rows * blocks * 16, false, 16},
       {scales, sizes_bad ? 1 : rows * blocks, false, 1},
-      {x, sizes_bad ? 1 : extent(rows, x_stride, cols, z), true, z}};
+      matrix(x, sizes_bad, rows, x_stride, cols, z, true)};
   if (any_null(all)) return A2AV_ERR_NULLPTR;
   if (!is_float(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
   if (sizes_bad || bad_addresses(all)) return A2AV_ERR_INVALID_ARGS;
@@ -411,7 +469,7 @@ int a2av_moe_gmm_mx4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t x_
       {w_scales, sizes_bad ? 1 : E * N * blocks, false, 1},
       {counts, sizes_bad ? 1 : int64_t(E) * 4, false, 4},
       {index, sizes_bad ? 1 : rows * 4, false, 4, true},
-      {y, sizes_bad ? 1 : extent(rows, y_stride, N, z), true, z},
+      matrix(y, sizes_bad, rows, y_stride, N, z, true),
       {status, 4, true, 4, true}};
   if (some && any_null(all)) return A2AV_ERR_NULLPTR;
   if (!is_float(y_dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;

@@ -14,7 +14,8 @@
  *   - Host checks run before anything is enqueued, in this order: NULLPTR (a
  *     required pointer is NULL; a pointer to an operand without bytes may be
  *     NULL) -> UNSUPPORTED_DTYPE -> INVALID_ARGS (sizes, strides, alignment,
- *     an output that shares a byte with another operand).  A failed launch is
+ *     an output that shares a byte with another operand; rows of one may lie
+ *     between another's, as columns of one buffer do).  A failed launch is
  *     A2AV_ERR_HIP.
  *   - `status` is a device int32 that may be NULL.  The device writes it only
  *     when a check on device data fails (the codes of a2av.h), so it is a

@@ -1,0 +1,43 @@
+"""CPU tests of what the operators accept and refuse as operands: shared bytes of
+strided rows, against a count of the bytes one by one."""
+import random
+
+import pytest
+import torch
+
+from all_movement_amd import a2av
+from tests.test_moe_host import A, INVALID, call
+
+
+def _bytes(at, rows, stride, width):
+    return {at + r * stride + b for r in range(rows) for b in range(width)}
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="accepted calls would be launched")
+def test_an_output_may_interleave_with_another_operand_but_share_no_byte():
+    """x and y of one buffer: refused exactly if they share a byte."""
+    rng = random.Random(5)
+    seen = [0, 0]
+    for _ in range(6000):
+        rows, x_rows = rng.randint(1, 7), 0
+        x_rows = rows + rng.randint(0, 3)
+        K, N = rng.randint(1, 9), rng.randint(1, 9)
+        xs = K + rng.choice([0, 1, 5, 12, 30])
+        ys = xs if rng.random() < 0.4 and xs >= N else N + rng.choice([0, 2, 9, 31])
+        y = A[0] + 2 * rng.randint(-rows * ys - 3, x_rows * xs + 3)
+        shared = bool(_bytes(A[0], x_rows, 2 * xs, 2 * K) & _bytes(y, rows, 2 * ys, 2 * N))
+        got = call("a2av_moe_gmm", x=A[0], x_stride=xs, x_rows=x_rows, y=y, y_stride=ys, rows=rows,
+                   N=N, K=K, w=A[8], status=None)
+        assert (got == INVALID) == shared, (rows, x_rows, K, N, xs, ys, y - A[0])
+        seen[shared] += 1
+    assert min(seen) > 500
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="accepted calls would be launched")
+def test_halves_of_one_buffer_are_accepted():
+    half = dict(y=A[0], y_stride=128, out=A[0] + 128, out_stride=128, width=64)
+    assert call("a2av_moe_combine", **half) != INVALID
+    assert call("a2av_moe_combine", **{**half, "out": A[0] + 126}) == INVALID
+    # Far rows: strides and extents of the largest sizes.
+    far = dict(rows=2 ** 30, cols=2 ** 30, x=A[0], x_stride=2 ** 31 - 1, dtype=a2av.FP32)
+    assert call("a2av_moe_mx4_dequantize", **{**far, "codes": A[1], "scales": A[2]}) == INVALID
