@@ -480,7 +480,9 @@ __global__ __launch_bounds__(256) void route_back(const RouteBackParams p) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         q[i] *= inverse;
-        gr[i] = q[i] == 0.0f ? 0.0f : q[i] * (gr[i] - mean);
+        // -inf is asked for by itself: beside a NaN its q, 0 times NaN, is not 0.
+        const bool none = row.v[i] == -__builtin_inff() || q[i] == 0.0f;
+        gr[i] = none ? 0.0f : q[i] * (gr[i] - mean);
       }
     }
     Row<PER>::store(p.dlogits, t * p.E, p.E, p.dtype, vec_out, gr);
