@@ -1266,13 +1266,22 @@ __global__ __launch_bounds__(NW * 64, 4) void gmm_few(const GmmParams p) {
   const uint8_t* w[FN];
   const uint8_t* xs[TY == kGmmMX4 ? MT : 1];
   const uint8_t* ws[TY == kGmmMX4 ? FN : 1];
+  // A row outside x reads row 0 and is made zeros before the products, as in the
+  // tile kernels, so that W's NaN and infinities show in it with every kernel.
+  int mask[MT];
+  bool bad_row = false;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int r = i * 16 + l16;
     int64_t row = t.span.row0 + (r < t.rm ? r : t.rm - 1);
-    if (p.index) {  // a row outside x reads row 0; its sums are dropped below
+    mask[i] = -1;
+    if (p.index) {
       row = p.index[row];
-      row = row >= 0 && row < p.x_rows ? row : 0;
+      if (row < 0 || row >= p.x_rows) {
+        row = 0;
+        mask[i] = 0;
+        bad_row = true;
+      }
     }
     x[i] = p.rows + row * p.row_stride + g * 16;
     if constexpr (TY == kGmmMX4) xs[i] = p.row_scales + row * p.blocks;
@@ -1347,14 +1356,16 @@ __global__ __launch_bounds__(NW * 64, 4) void gmm_few(const GmmParams p) {
 #pragma unroll
     for (int u = 0; u < kN; ++u)
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < MT; ++i) {
+        const int4v row = xv[u][i] & mask[i];
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
-          if constexpr (TY == kGmmMX4)
-            acc[i][f] = mma_mx4(wv[u][f], xv[u][i], acc[i][f], wsv[u][f], xsv[u][i], 0);
+          if constexpr (TY == kGmmMX4)  // row 0's scale may be NaN
+            acc[i][f] = mma_mx4(wv[u][f], row, acc[i][f], wsv[u][f], xsv[u][i] & mask[i], 0);
           else
-            acc[i][f] = mma<TY>(wv[u][f], xv[u][i], acc[i][f]);
+            acc[i][f] = mma<TY>(wv[u][f], row, acc[i][f]);
         }
+      }
     end_of_products();
   };
   // Waves take groups of U steps in turn.
@@ -1364,6 +1375,7 @@ __global__ __launch_bounds__(NW * 64, 4) void gmm_few(const GmmParams p) {
     run(s, std::integral_constant<int, U>{}, std::false_type{});
   for (int s = whole + wave; s < steps; s += NW)
     run(s, std::integral_constant<int, 1>{}, std::true_type{});
+  if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
 
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -1379,13 +1391,6 @@ __global__ __launch_bounds__(NW * 64, 4) void gmm_few(const GmmParams p) {
     float v = 0.0f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) v += part[i][(r >> 4) * FN + (c >> 4)][at];
-    if (p.index) {
-      const int64_t row = p.index[t.span.row0 + r];
-      if (row < 0 || row >= p.x_rows) {
-        v = 0.0f;
-        if (p.status) *p.status = A2AV_ERR_INVALID_ARGS;
-      }
-    }
     const int64_t o = (t.out_row0 + r) * p.out_stride + t.c0 + c;
     if (p.out_type == A2AV_FP32)
       reinterpret_cast<float*>(p.out)[o] = v;

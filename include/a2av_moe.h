@@ -98,7 +98,8 @@ int a2av_moe_route_backward(const void *logits, int64_t logits_stride, int64_t t
  * without rows gets dW = 0.
  * Device checks: a negative count, or counts that sum to more than `rows` ->
  * INVALID_ARGS, nothing written; an index in use outside [0, x_rows) ->
- * INVALID_ARGS, and that row counts as a row of zeros.
+ * INVALID_ARGS, and that row counts as a row of zeros: its y is 0, or NaN where
+ * W holds a NaN or an infinity (in dW, where dy does).
  * Limits: rows, x_rows, N, K <= 2^30, E in 1..4096.
  */
 int a2av_moe_gmm(const void *x, int64_t x_stride, int64_t x_rows, const void *w,

@@ -1,10 +1,11 @@
-"""Operands at the border of what the operators take."""
+"""Operands at the border of what the operators take: interleaved views, logits
+that are no numbers beside masked ones, indexes outside x in every kernel."""
 import math
 
 import pytest
 import torch
 
-from all_movement_amd import moe
+from all_movement_amd import a2av, moe
 from tests import moe_plain as plain
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +61,83 @@ def test_gradient_of_masked_logits_beside_ones_that_are_no_numbers(dt, renorm, E
     off = (d[rest].double().cpu() - want).abs()
     assert bool((off <= tol + plain.step(dt) * want.abs() +
                  torch.finfo(dt).smallest_normal * torch.finfo(dt).eps).all())
+
+
+def same(a, b):
+    return torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
+# Sizes that take each forward kernel: few rows per expert (16 and 32 rows to a
+# tile), 128 x 128 tiles with four and with two stages, 256 x 256 tiles cut and
+# whole, loads by way of registers in 64 x 64 and 128 x 128 tiles, short rows.
+KERNELS = [([3, 5], 32, 64), ([20, 9], 72, 77), ([30, 40], 40, 1000), ([100, 60], 264, 640),
+           ([30 + 3 * i for i in range(24)], 2176, 512), ([300, 200], 264, 640),
+           ([520, 300], 16640, 640), ([90, 70], 64, 203), ([2048], 4199, 203), ([60, 60], 24, 5)]
+
+
+def bad_index(counts, tokens, spread, gen):
+    """An index whose bad entries lie in the rows that one wave loads (or all
+    over), and the same with them on row `tokens` (zeros)."""
+    rows = sum(counts)
+    index = torch.randint(1, tokens, (rows,), generator=gen).to(torch.int32)
+    at = list(range(0, rows, 5)) if spread else [rows // 3]
+    fixed = index.clone()
+    for i, a in enumerate(at):
+        index[a] = (-1, tokens, 2 ** 31 - 1, -2 ** 31)[i % 4]
+        fixed[a] = tokens
+    return index.to(DEV), fixed.to(DEV)
+
+
+@pytest.mark.parametrize("counts,N,K", KERNELS)
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("finite", [True, False])
+def test_rows_outside_x_are_rows_of_zeros(counts, N, K, spread, finite):
+    gen = torch.Generator().manual_seed(N + K)
+    E, tokens, dt = len(counts), 50, torch.bfloat16
+    x = torch.randn(tokens, K, generator=gen).to(dt).to(DEV)
+    x[0] = math.nan  # nobody's row
+    x0 = torch.cat([x, torch.zeros_like(x[:1])])
+    w = torch.randn(E, N, K, device=DEV, dtype=dt)
+    dy = torch.randn(sum(counts), N, device=DEV, dtype=dt)
+    if not finite:  # zeros times these are NaN
+        w[E - 1, N // 2, K - 1] = math.inf
+        w[0, 0, 0] = math.nan
+        dy[sum(counts) // 3, N - 1] = math.inf
+    c = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    index, fixed = bad_index(counts, tokens, spread, gen)
+    print("bad index", counts[:4], N, K, spread, finite, flush=True)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = moe.gmm(x, w, c, index=index, status=status)
+    assert status.item() == a2av.ERR_INVALID_ARGS
+    assert same(y, moe.gmm(x0, w, c, index=fixed, check=True))
+    status.zero_()
+    dw = moe.gmm_dw(dy, x, c, index=index, status=status)
+    assert status.item() == a2av.ERR_INVALID_ARGS
+    assert same(dw, moe.gmm_dw(dy, x0, c, index=fixed, check=True))
+
+
+# The 4-bit kernels: whole scale groups (K of 512) and others.
+@pytest.mark.parametrize("counts,N,K", [
+    ([3, 5], 32, 64), ([30, 40], 40, 1000), ([20, 9], 72, 1024), ([100, 60], 264, 1536),
+    ([30 + 3 * i for i in range(24)], 2176, 1024), ([300, 200], 264, 2560),
+    ([520, 300], 16640, 1024), ([90, 70], 64, 416)])
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("finite", [True, False])
+def test_4_bit_rows_outside_x_are_rows_of_zeros(counts, N, K, spread, finite):
+    gen = torch.Generator().manual_seed(N + K)
+    E, tokens, B = len(counts), 50, (K + 31) // 32
+    xc, xs = moe.mx4_quantize(torch.randn(tokens, K, generator=gen).to(DEV))
+    xs[0] = 255  # nobody's row
+    zc, zs = moe.mx4_quantize(torch.zeros(1, K, device=DEV))
+    x0c, x0s = torch.cat([xc, zc]), torch.cat([xs, zs])
+    wc, ws = moe.mx4_quantize(torch.randn(E * N, K, device=DEV))
+    wc, ws = wc.view(E, N, 16 * B), ws.view(E, N, B)
+    if not finite:
+        ws[E - 1, N // 2, B - 1] = 255
+    c = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    index, fixed = bad_index(counts, tokens, spread, gen)
+    print("bad index, 4 bits", counts[:4], N, K, spread, finite, flush=True)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = moe.gmm_mx4(xc, xs, wc, ws, c, index=index, status=status, dtype=torch.float32)
+    assert status.item() == a2av.ERR_INVALID_ARGS
+    assert same(y, moe.gmm_mx4(x0c, x0s, wc, ws, c, index=fixed, check=True, dtype=torch.float32))
