@@ -13,6 +13,11 @@ tensors' device and on ``stream`` (default: torch's current stream there, which
 is also the stream that outputs are allocated for).  ``status``, an int32
 tensor of one element, receives the code of a check on device data that failed
 (it is never cleared); with ``check=True`` the call waits and raises instead.
+
+Gradients are calls of their own (``route_backward``, ``gmm_dx``, ``gmm_dw``,
+``combine_backward``), for a training step or an autograd function to make; no
+call records one, so that operands that require a gradient are refused unless
+recording is off (``torch.no_grad()``).
 """
 from __future__ import annotations
 
@@ -102,10 +107,16 @@ def _whole(t, name: str, shape, dtype):
 
 
 def _device(*named):
-    dev = named[0].device
+    first = named[0]
+    dev = first.device
     for t in named:
-        if t is not None and t is not named[0] and t.device != dev:
+        if t is None:
+            continue
+        if t is not first and t.device != dev:
             raise ValueError(f"operands on {dev} and {t.device}")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("an operand requires a gradient, which no call here records: the "
+                             "gradients are calls of their own (use detach or torch.no_grad)")
     if dev.type != "cuda":
         raise ValueError(f"operands must live on a GPU, not {dev}")
     return dev

@@ -5,7 +5,7 @@ import random
 import pytest
 import torch
 
-from all_movement_amd import a2av
+from all_movement_amd import a2av, moe
 from tests.test_moe_host import A, INVALID, call
 
 
@@ -41,3 +41,27 @@ def test_halves_of_one_buffer_are_accepted():
     # Far rows: strides and extents of the largest sizes.
     far = dict(rows=2 ** 30, cols=2 ** 30, x=A[0], x_stride=2 ** 31 - 1, dtype=a2av.FP32)
     assert call("a2av_moe_mx4_dequantize", **{**far, "codes": A[1], "scales": A[2]}) == INVALID
+
+
+def test_a_gradient_is_not_lost_in_silence():
+    """No call records a gradient: operands that want one are refused while
+    gradients are recorded."""
+    x, w = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(2, 8, 16, dtype=torch.bfloat16)
+    c, p = torch.zeros(2, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.int32)
+    f = torch.zeros(4, 2)
+
+    def g(t):
+        return t.clone().requires_grad_()
+    calls = [lambda: moe.gmm(g(x), w, c), lambda: moe.gmm(x, g(w), c),
+             lambda: moe.gmm_dx(g(x[:, :8].contiguous()), w, c),
+             lambda: moe.gmm_dw(x, g(x), c), lambda: moe.route(g(f), 1),
+             lambda: moe.route_backward(f, p[:, :1].contiguous(), g(f[:, :1].contiguous()),
+                                        f[:, :1].contiguous()),
+             lambda: moe.combine(g(x), p, f), lambda: moe.combine(x, p, g(f)),
+             lambda: moe.combine_backward(x, g(x), p, f), lambda: moe.mx4_quantize(g(x)),
+             lambda: moe.combine(x, p, f, out=g(x))]
+    for one in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            one()
+        with torch.no_grad(), pytest.raises(ValueError, match="must live on a GPU"):
+            one()
