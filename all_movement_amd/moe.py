@@ -10,9 +10,11 @@ Every step runs in the HIP library.  Nothing is converted or copied: a tensor
 that would need it is refused.  Rows may be strided, everything else is
 contiguous.  Outputs that are not given are allocated; the work runs on the
 tensors' device and on ``stream`` (default: torch's current stream there, which
-is also the stream that outputs are allocated for).  ``status``, an int32
-tensor of one element, receives the code of a check on device data that failed
-(it is never cleared); with ``check=True`` the call waits and raises instead.
+is also the stream that outputs are allocated for).  As under
+``torch.cuda.stream``, the order and the lifetime of operands across streams are
+the caller's.  ``status``, an int32 tensor of one element, receives the code of a
+check on device data that failed (it is never cleared); with ``check=True`` the
+call waits and raises instead.
 
 Gradients are calls of their own (``route_backward``, ``gmm_dx``, ``gmm_dw``,
 ``combine_backward``), for a training step or an autograd function to make; no
@@ -124,7 +126,11 @@ def _device(*named):
 
 def _elsewhere(dev, stream) -> bool:
     """Whether the call has to be made under another device or stream."""
-    return stream is not None or torch._C._cuda_getDevice() != dev.index
+    if stream is None:
+        return torch._C._cuda_getDevice() != dev.index
+    if stream.device != dev:
+        raise ValueError(f"stream of {stream.device} for operands on {dev}")
+    return True
 
 
 @contextlib.contextmanager

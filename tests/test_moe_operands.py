@@ -1,6 +1,7 @@
 """CPU tests of what the operators accept and refuse as operands: shared bytes of
 strided rows, against a count of the bytes one by one."""
 import random
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -65,3 +66,10 @@ def test_a_gradient_is_not_lost_in_silence():
             one()
         with torch.no_grad(), pytest.raises(ValueError, match="must live on a GPU"):
             one()
+
+
+def test_a_stream_of_another_device_is_refused():
+    here, there = torch.device("cuda:0"), torch.device("cuda:1")
+    with pytest.raises(ValueError, match="stream"):
+        moe._elsewhere(here, SimpleNamespace(device=there))
+    assert moe._elsewhere(here, SimpleNamespace(device=here))
