@@ -43,7 +43,7 @@ __device__ inline void load_to_lds(const uint8_t* src, uint32_t base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(base), "v"(src)
-               : "memory", "m0");
+               : "memory");
 }
 
 __device__ inline void wait_loads_and_barrier() {
@@ -754,7 +754,7 @@ __device__ inline void load_to_lds(const uint8_t* base, uint32_t offset, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(to), "v"(offset), "s"(base)
-               : "memory", "m0");
+               : "memory");
 }
 
 // 4 bytes per lane from `src` to LDS at base + 4 * lane.
@@ -762,7 +762,7 @@ __device__ inline void load_word_to_lds(const void* src, uint32_t base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :
                : "s"(base), "v"(src)
-               : "memory", "m0");
+               : "memory");
 }
 
 template <class T>
