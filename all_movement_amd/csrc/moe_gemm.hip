@@ -1433,16 +1433,18 @@ hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
       return launch_tiles<MODE, 32, 32>(gmm_few<TY, 2, 2, kWaves>, kWaves * 64, p, stream);
   }
   if (direct) {
-    const int64_t cols = MODE == kGmmFwd ? p.N : p.K;
-    const int64_t used = p.E < p.nrows ? p.E : p.nrows;
     // Rows of an expert (dw: of the reduction, which no tile cuts).
-    const bool large = MODE == kGmmDw || p.nrows / p.E >= 160;
-    if (large) return launch_tiles<MODE, 256, 256>(gmm_large<TY, MODE>, 256, p, stream);
-    // Tiles for every CU: two workgroups on each hide each other's ends.  Fewer:
-    // one, with four stages of loads in flight.
-    if ((p.nrows / 128 + used / 2) * ((cols + 127) / 128) > 384)
-      return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 2>, 256, p, stream);
-    return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 4>, 256, p, stream);
+    if (MODE == kGmmDw || p.nrows / p.E >= 160)
+      return launch_tiles<MODE, 256, 256>(gmm_large<TY, MODE>, 256, p, stream);
+    if constexpr (MODE != kGmmDw) {
+      const int64_t cols = MODE == kGmmFwd ? p.N : p.K;
+      const int64_t used = p.E < p.nrows ? p.E : p.nrows;
+      // Tiles for every CU: two workgroups on each hide each other's ends.  Fewer:
+      // one, with four stages of loads in flight.
+      if ((p.nrows / 128 + used / 2) * ((cols + 127) / 128) > 384)
+        return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 2>, 256, p, stream);
+      return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 4>, 256, p, stream);
+    }
   }
   if constexpr (TY != kGmmMX4) {
     if (p.K < 8 || (MODE != kGmmFwd && p.N < 8))  // rows of an operand

@@ -356,10 +356,10 @@ hipError_t launch_combine(const CombineParams& p, hipStream_t stream) {
       const int64_t wgs = (int64_t(p.tokens) * across + 255) / 256;
       const int cols = (pieces + across - 1) / across;
       const dim3 grid(uint32_t(wgs < (1 << 20) ? wgs : (1 << 20)), uint32_t(cols < 64 ? cols : 64));
-      if (across >= 64)
-        combine_kernel<DT, N, kAligned, true><<<grid, dim3(256), 0, stream>>>(p, across);
-      else
-        combine_kernel<DT, N, kAligned, false><<<grid, dim3(256), 0, stream>>>(p, across);
+      if constexpr (N > 1)  // single elements: rows of fewer than 8
+        if (across >= 64)
+          return combine_kernel<DT, N, kAligned, true><<<grid, dim3(256), 0, stream>>>(p, across);
+      combine_kernel<DT, N, kAligned, false><<<grid, dim3(256), 0, stream>>>(p, across);
     });
   });
 }
@@ -373,10 +373,10 @@ hipError_t launch_combine_back(const CombineParams& p, hipStream_t stream) {
     with_pieces<DT>(fast, p.width, [&](auto n, auto is_aligned) {
       constexpr int N = decltype(n)::value;
       constexpr bool kAligned = decltype(is_aligned)::value;
-      if ((p.width + N - 1) / N <= 64)
-        combine_back_kernel<DT, N, kAligned, 64><<<grid, dim3(64), 0, stream>>>(p);
-      else
-        combine_back_kernel<DT, N, kAligned, 256><<<grid, dim3(256), 0, stream>>>(p);
+      if constexpr (N > 1)
+        if ((p.width + N - 1) / N > 64)
+          return combine_back_kernel<DT, N, kAligned, 256><<<grid, dim3(256), 0, stream>>>(p);
+      combine_back_kernel<DT, N, kAligned, 64><<<grid, dim3(64), 0, stream>>>(p);
     });
   });
 }
