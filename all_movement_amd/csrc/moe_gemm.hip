@@ -1423,24 +1423,53 @@ hipError_t launch_tiles(Kernel kernel, int threads, const GmmParams& p, hipStrea
 template <int TY, int MODE>
 hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
   if constexpr (MODE == kGmmFwd) {
-    // By the mean rows of an expert (the counts stay on the device).  A row of 4
-    // bits is a quarter as long: fewer waves share it out.
+    // The streaming kernel reads W once per row tile: it pays while the rows of an
+    // expert mostly fit into one tile, and otherwise while its workgroups (an
+    // estimate: the counts stay on the device) are all on the CUs at once, 8 waves
+    // to each.  A row of 4 bits is a quarter as long: fewer waves share it out.
+    // us against the tile kernel that it would be, bf16: 64 experts of 2048 x 2048,
+    // 8 rows each 104 and 136, 12 rows 113 and 136, 16 rows 141 and 136, 24 rows 179
+    // and 137; 8 of 2048 x 7168, 12 rows 52 and 59, 16 rows (32 to a tile, 512
+    // workgroups) 63 and 59; 4 of those, 24 rows (256) 41 and 54; one, 40 rows (192)
+    // 24 and 46.  Half of 640 rows on one of the 64 experts: 120 and 136.
+    // One expert of 256 x 4096, 512 rows (256) 15 and 30, 2048 rows 46 and 30.
+    // Unaligned rows, 2001 x 7001, 8 rows: 8 experts (504) 94 and 72, one (63) 48 and
+    // 57; 32 to a tile, 257 x 4001, 512 rows (144) 42 and 35.  4 bits, 64 of 2048 x 2048, 12 rows 35 and 36, 16 rows 42 and 37; 8 of
+    // 2048 x 7168, 24 rows (512) 18 and 24, 40 rows (1024) 30 and 25.  Against the
+    // slower kernel of other scale groups, 2048 x 7200: 40 rows 34 and 49, 64 rows
+    // (1536) 42 and 51; 64 of 2048 x 1408, 32 rows (8192) 44 and 37.
     constexpr int kWaves = TY == kGmmMX4 ? 4 : 8;
-    const bool rows = p.x_rows > 0;  // the streaming kernel reads row 0 for rows outside x
-    if (rows && p.nrows <= int64_t(p.E) * 12)
-      return launch_tiles<MODE, 16, 32>(gmm_few<TY, 1, 2, kWaves>, kWaves * 64, p, stream);
-    if (rows && p.nrows <= int64_t(p.E) * 40)
-      return launch_tiles<MODE, 32, 32>(gmm_few<TY, 2, 2, kWaves>, kWaves * 64, p, stream);
+    const int64_t used = p.E < p.nrows ? p.E : p.nrows;
+    const auto workgroups = [&](int BM) {
+      const int64_t mean = (p.nrows + used - 1) / used;
+      const int64_t most = used == 1 ? mean : mean + mean / 3;  // rows of most experts
+      return used * ((most + BM - 1) / BM) * ((int64_t(p.N) + 31) / 32);
+    };
+    constexpr int64_t kAtOnce = 256 * 8 / kWaves;
+    if (p.x_rows > 0) {  // it reads row 0 for rows outside x
+      const bool one_tile = p.nrows <= int64_t(p.E) * 12 && (direct || TY == kGmmMX4);
+      if (one_tile || workgroups(16) <= kAtOnce)
+        return launch_tiles<MODE, 16, 32>(gmm_few<TY, 1, 2, kWaves>, kWaves * 64, p, stream);
+      if (workgroups(32) <= (direct ? kAtOnce : TY == kGmmMX4 ? 3 * kAtOnce : 0))
+        return launch_tiles<MODE, 32, 32>(gmm_few<TY, 2, 2, kWaves>, kWaves * 64, p, stream);
+    }
   }
   if (direct) {
-    // Rows of an expert (dw: of the reduction, which no tile cuts).
+    // Rows of an expert (dw: of the reduction, which no tile cuts).  us of the large
+    // tiles and the small ones, bf16, 64 experts of 2048 x 2048: 96 rows each 155 and
+    // 141, dx 139 and 119; 128 rows 157 and 158, 142 and 145; 160 rows 161 and 178,
+    // 144 and 176.  8 experts of 2048 x 7168: 96 rows 79 and 79, dx 66 and 56; 160 rows
+    // 83 and 83, 68 and 84.
     if (MODE == kGmmDw || p.nrows / p.E >= 160)
       return launch_tiles<MODE, 256, 256>(gmm_large<TY, MODE>, 256, p, stream);
     if constexpr (MODE != kGmmDw) {
       const int64_t cols = MODE == kGmmFwd ? p.N : p.K;
       const int64_t used = p.E < p.nrows ? p.E : p.nrows;
       // Tiles for every CU: two workgroups on each hide each other's ends.  Fewer:
-      // one, with four stages of loads in flight.
+      // one, with four stages of loads in flight.  us of two stages and four, bf16, 64
+      // rows of each expert, 2048 x 2048: 16 experts (256 tiles) 43 and 40, dx 40 and
+      // 35; 32 experts (512) 73 and 75, 60 and 63.  24 of 4096 x 2048 (768): 113 and
+      // 107, 93 and 90; 8 of 2048 x 7168 (128): 103 and 71.
       if ((p.nrows / 128 + used / 2) * ((cols + 127) / 128) > 384)
         return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 2>, 256, p, stream);
       return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 4>, 256, p, stream);
@@ -1454,7 +1483,11 @@ hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
     const int64_t cols = ((MODE == kGmmFwd ? p.N : p.K) + 127) / 128;
     const int64_t rows = MODE == kGmmDw ? int64_t(p.E) * ((p.N + 127) / 128)
                                         : p.nrows / 128 + used / 2;
-    // Too few tiles for two on every CU: quarters of them.
+    // Too few tiles for two on every CU: quarters of them.  us of 64 x 64 tiles and
+    // of 128 x 128, bf16: 8 experts of 256 rows, 2001 x 1003 (320 tiles), 35 and 43, dx
+    // 34 and 45; 512 rows (576) 55 and 63, 54 and 65; 16 of 300 rows, 2001 x 2003 (720)
+    // 156 and 118, 158 and 121.  dw, 8 of 256 rows: 1001 x 1003 (512) 24 and 26, 2001 x
+    // 2003 (2048) 76 and 88; of 4096 rows 789 and 782; one of 8192, 4001 x 4003: 775, 719.
     if (rows * cols < 512)
       return launch_tiles<MODE, 64, 64>(gmm_kernel<TY, MODE, 64, 64, 2, 2, false>, 256, p, stream);
   }

@@ -146,3 +146,22 @@ def test_4_bit_rows(counts, N, K, tokens):
         want = x[at:at + m] @ values(wc[e], ws[e]).t()
         assert torch.equal(y[at:at + m], want.float()), f"expert {e}"
         at += m
+
+
+# Few workgroups of the streaming kernel: few experts or few columns, with 16 and
+# with 32 rows to a tile, and many tiles of one expert.
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("counts,N,K,tokens", [
+    ([20, 20, 20, 20, 0, 31, 9, 40], 1024, 1048, None), ([18, 22, 0, 24], 2040, 264, 60),
+    ([600], 256, 4096, 99), ([500], 250, 1024, None), ([40], 2048, 1032, None),
+    ([7, 0, 3], 131, 1003, 9), ([300], 61, 397, 30), ([90, 0, 33], 64, 2048, 70)])
+def test_streamed_rows(dt, counts, N, K, tokens):
+    check(counts, N, K, dt, tokens, ("fwd",))
+
+
+@pytest.mark.parametrize("counts,N,K,tokens", [
+    ([20, 20, 20, 20, 0, 31, 9, 40], 2048, 1024, None), ([24, 0, 22, 18], 4096, 2560, 50),
+    ([40, 50, 0, 60, 30, 40, 50, 44], 2048, 1056, 77), ([2000], 256, 2560, 300),
+    ([1500], 256, 1056, None), ([33], 2048, 2880, None)])
+def test_streamed_4_bit_rows(counts, N, K, tokens):
+    test_4_bit_rows(counts, N, K, tokens)

@@ -141,3 +141,18 @@ def test_4_bit_rows_outside_x_are_rows_of_zeros(counts, N, K, spread, finite):
     y = moe.gmm_mx4(xc, xs, wc, ws, c, index=index, status=status, dtype=torch.float32)
     assert status.item() == a2av.ERR_INVALID_ARGS
     assert same(y, moe.gmm_mx4(x0c, x0s, wc, ws, c, index=fixed, check=True, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("counts,N,K", [([20] * 8, 1024, 520), ([500], 250, 1024), ([300], 61, 397)])
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("finite", [True, False])
+def test_streamed_rows_outside_x_are_rows_of_zeros(counts, N, K, spread, finite):
+    test_rows_outside_x_are_rows_of_zeros(counts, N, K, spread, finite)
+
+
+@pytest.mark.parametrize("counts,N,K", [([20] * 8, 2048, 1024), ([50] * 8, 2048, 1056),
+                                        ([2000], 256, 512)])
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("finite", [True, False])
+def test_streamed_4_bit_rows_outside_x_are_rows_of_zeros(counts, N, K, spread, finite):
+    test_4_bit_rows_outside_x_are_rows_of_zeros(counts, N, K, spread, finite)
