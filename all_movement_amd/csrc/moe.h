@@ -1,4 +1,4 @@
-// moe.h -- what the host checks (moe_host.cpp) hand to the kernels of the
+// moe.h -- what the host checks (moe_host.hip) hand to the kernels of the
 // operators around the exchange (moe_gemm.hip, moe_route.hip, moe_rows.hip).
 #pragma once
 

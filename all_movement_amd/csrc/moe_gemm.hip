@@ -5,12 +5,17 @@
 //   forward  y [r][n] = sum_k x[index[r]][k] W[e][n][k]
 //   dx       dx[r][k] = sum_n dy[r][n] W[e][n][k]
 //   dw       dW[e][n][k] = sum_r dy[r][n] x[index[r]][k]
-// One tile kernel computes all three: a BM x BN tile of the output in FP32
-// accumulators, 128 bytes of the reduction (64 elements of 16 bits, 256 of 4)
-// per step through two LDS buffers.  An operand is "along" when the reduction
-// runs along its rows (x, dy, and W in the forward product) and "across" when
-// it runs over its rows (W in dx, both in dw); an across tile is read from LDS
-// with the transposing read, so no operand is ever transposed in memory.
+// Each kernel sums in FP32:
+//   gmm_large, gmm_small  256 x 256 and 128 x 128 tiles of the output, 128 bytes of
+//       the reduction (64 elements of 16 bits, 256 of 4) per stage, brought straight
+//       to LDS: rows whose pieces of 16 bytes are aligned
+//   gmm_kernel  64 x 64 and 128 x 128 tiles with loads by way of registers: every
+//       alignment and stride; in 4 bits straight to LDS, for any number of blocks
+//   gmm_few  few rows per expert, forward: W streams into registers
+// An operand is "along" when the reduction runs along its rows (x, dy, and W in
+// the forward product) and "across" when it runs over its rows (W in dx, both in
+// dw); a tile kernel reads an across tile from LDS with the transposing read, so
+// no operand is ever transposed in memory.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -846,11 +851,11 @@ __device__ inline void mma_acc(float4v& acc, int4v a, int4v b, int sa, int sb) {
 #undef A2AV_MMA
 
 // BM x BN of the output by WM x WN waves, one per SIMD, 128 bytes of the
-// reduction (64 elements of 16 bits, 256 of 4) per stage, through two LDS
+// reduction (64 elements of 16 bits, 256 of 4) per stage, through NB LDS
 // buffers.  A stage has two halves of 64 bytes.  While a wave multiplies the
 // fragments of one half it reads those of the next into other registers.  Once
 // the second half's are read stands the stage's one barrier: past it nobody
-// reads the stage's buffer again, and the loads of stage s + 2 go there; before
+// reads the stage's buffer again, and the loads of stage s + NB go there; before
 // it everybody waits for his loads of stage s + 1.
 // Loads past the last stage read zeros.  Every row of every operand begins and
 // ends on a 16-byte chunk, and the rows that a tile reads lie within 4 GiB of
@@ -1013,7 +1018,7 @@ __device__ inline void gmm_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
     }
   };
 
-  // ---- load i of stage s, into buffer s % 2.  FAST: all of it exists.
+  // ---- load i of stage s, into buffer s % NB.  FAST: all of it exists.
   auto load_one = [&](int s, int i, auto fast) {
     const bool is_q = i < kQ;
     const uint32_t to = lds0 + s % NB * kBuf +
@@ -1420,37 +1425,51 @@ hipError_t launch_tiles(Kernel kernel, int threads, const GmmParams& p, hipStrea
   return hipGetLastError();
 }
 
+// Row tiles of nrows rows, about: the counts stay on the device, and most experts
+// are taken to have up to a third more rows than the mean.
+int64_t expected_row_tiles(const GmmParams& p, int BM) {
+  const int64_t used = p.E < p.nrows ? p.E : p.nrows;
+  const int64_t mean = (p.nrows + used - 1) / used;
+  const int64_t most = p.E == 1 ? mean : mean + mean / 3;
+  return used * ((most + BM - 1) / BM);
+}
+
 template <int TY, int MODE>
 hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
   if constexpr (MODE == kGmmFwd) {
     // The streaming kernel reads W once per row tile: it pays while the rows of an
-    // expert mostly fit into one tile, and otherwise while its workgroups (an
-    // estimate: the counts stay on the device) are all on the CUs at once, 8 waves
-    // to each.  A row of 4 bits is a quarter as long: fewer waves share it out.
-    // us against the tile kernel that it would be, bf16: 64 experts of 2048 x 2048,
-    // 8 rows each 104 and 136, 12 rows 113 and 136, 16 rows 141 and 136, 24 rows 179
-    // and 137; 8 of 2048 x 7168, 12 rows 52 and 59, 16 rows (32 to a tile, 512
-    // workgroups) 63 and 59; 4 of those, 24 rows (256) 41 and 54; one, 40 rows (192)
-    // 24 and 46.  Half of 640 rows on one of the 64 experts: 120 and 136.
-    // One expert of 256 x 4096, 512 rows (256) 15 and 30, 2048 rows 46 and 30.
-    // Unaligned rows, 2001 x 7001, 8 rows: 8 experts (504) 94 and 72, one (63) 48 and
-    // 57; 32 to a tile, 257 x 4001, 512 rows (144) 42 and 35.  4 bits, 64 of 2048 x 2048, 12 rows 35 and 36, 16 rows 42 and 37; 8 of
-    // 2048 x 7168, 24 rows (512) 18 and 24, 40 rows (1024) 30 and 25.  Against the
-    // slower kernel of other scale groups, 2048 x 7200: 40 rows 34 and 49, 64 rows
-    // (1536) 42 and 51; 64 of 2048 x 1408, 32 rows (8192) 44 and 37.
-    constexpr int kWaves = TY == kGmmMX4 ? 4 : 8;
-    const int64_t used = p.E < p.nrows ? p.E : p.nrows;
-    const auto workgroups = [&](int BM) {
-      const int64_t mean = (p.nrows + used - 1) / used;
-      const int64_t most = used == 1 ? mean : mean + mean / 3;  // rows of most experts
-      return used * ((most + BM - 1) / BM) * ((int64_t(p.N) + 31) / 32);
+    // expert mostly fit into one tile, and otherwise while about one workgroup is on
+    // every CU (4 bits: two), more of them for short rows, whose products take less
+    // than a tile's start (as much as 1 KiB of a row; 512 bytes count at least).  Over
+    // some 700 sizes that it was not made with (1 to 64 experts of 3 to 60 rows, some
+    // with a hot one, N to 4096, K to 7168) the kernel chosen takes 1.01 to 1.03 times
+    // the fastest one's time in each of the four kinds below, and by 12 and 40 rows per
+    // expert alone 1.10 to 1.21.
+    // us of it and of the tile kernel in its place (in brackets its workgroups):
+    //   bf16, 64 experts of 2048 x 2048: 8 rows each 104 and 136, 12 rows 113 and 136,
+    //   16 rows 141 and 136, 24 rows 179 and 137; half of 640 rows on one expert 120
+    //   and 136.  8 of 2048 x 7168: 12 rows 52 and 59, 16 rows (512) 63 and 59; 4 of
+    //   them: 24 rows (256) 41 and 54; one: 40 rows (192) 24 and 46.  One of 256 x
+    //   4096: 512 rows (256) 15 and 30, 2048 rows (1024) 46 and 30.
+    //   Unaligned, 2001 x 7001, 8 rows: 8 experts (504) 94 and 72, one (63) 48 and 57;
+    //   257 x 4001, 512 rows in tiles of 32 (144) 42 and 35.
+    //   4 bits, 64 of 2048 x 2048: 12 rows 35 and 36, 24 rows 44 and 38; 8 of 2048 x
+    //   7168: 24 rows (512) 18 and 24, 40 rows (1024) 30 and 25.
+    //   4 bits of other scale groups, whose tile kernel is slower, 8 of 2048 x 7200: 40
+    //   rows (1024) 34 and 49, 64 rows (1536) 42 and 51; 64 of 2048 x 1408: 32 rows
+    //   (8192) 44 and 37.
+    constexpr int kWaves = TY == kGmmMX4 ? 4 : 8;  // a row of 4 bits is a quarter as long
+    const int64_t bytes = TY == kGmmMX4 ? p.K / 2 : p.K * int64_t(2);
+    const int64_t row = bytes < 512 ? 512 : bytes;
+    const auto at_once = [&](int BM, int limit) {
+      const int64_t wgs = expected_row_tiles(p, BM) * ((int64_t(p.N) + 31) / 32);
+      return wgs <= limit + (direct ? limit * 1024 / row : 0);
     };
-    constexpr int64_t kAtOnce = 256 * 8 / kWaves;
     if (p.x_rows > 0) {  // it reads row 0 for rows outside x
       const bool one_tile = p.nrows <= int64_t(p.E) * 12 && (direct || TY == kGmmMX4);
-      if (one_tile || workgroups(16) <= kAtOnce)
+      if (one_tile || at_once(16, 256))
         return launch_tiles<MODE, 16, 32>(gmm_few<TY, 1, 2, kWaves>, kWaves * 64, p, stream);
-      if (workgroups(32) <= (direct ? kAtOnce : TY == kGmmMX4 ? 3 * kAtOnce : 0))
+      if (at_once(32, TY == kGmmMX4 ? (direct ? 512 : 1536) : direct ? 256 : 0))
         return launch_tiles<MODE, 32, 32>(gmm_few<TY, 2, 2, kWaves>, kWaves * 64, p, stream);
     }
   }
@@ -1464,13 +1483,13 @@ hipError_t launch_mode(const GmmParams& p, bool direct, hipStream_t stream) {
       return launch_tiles<MODE, 256, 256>(gmm_large<TY, MODE>, 256, p, stream);
     if constexpr (MODE != kGmmDw) {
       const int64_t cols = MODE == kGmmFwd ? p.N : p.K;
-      const int64_t used = p.E < p.nrows ? p.E : p.nrows;
-      // Tiles for every CU: two workgroups on each hide each other's ends.  Fewer:
-      // one, with four stages of loads in flight.  us of two stages and four, bf16, 64
-      // rows of each expert, 2048 x 2048: 16 experts (256 tiles) 43 and 40, dx 40 and
-      // 35; 32 experts (512) 73 and 75, 60 and 63.  24 of 4096 x 2048 (768): 113 and
-      // 107, 93 and 90; 8 of 2048 x 7168 (128): 103 and 71.
-      if ((p.nrows / 128 + used / 2) * ((cols + 127) / 128) > 384)
+      // More tiles than CUs: two workgroups on each hide each other's ends.  Else one,
+      // with four stages of loads in flight.  us of two stages and four, bf16, 64 rows
+      // of each expert, 2048 x 2048: 16 experts (256 tiles) 43 and 40, dx 40 and 35; 32
+      // (512) 73 and 75, 60 and 63.  12 rows, 8 of 7168 x 2048 (448): 54 and 59, 4 bits
+      // (16 rows) 16 and 22; 32 of 4096 x 1024 (1024): 54 and 62.  8 of 2048 x 7168
+      // (128): 103 and 71.  24 of 4096 x 2048 (768), an exception: 113 and 107.
+      if (expected_row_tiles(p, 128) * ((cols + 127) / 128) > 256)
         return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 2>, 256, p, stream);
       return launch_tiles<MODE, 128, 128>(gmm_small<TY, MODE, 4>, 256, p, stream);
     }

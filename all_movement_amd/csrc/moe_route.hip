@@ -476,6 +476,8 @@ __global__ __launch_bounds__(256) void route_back(const RouteBackParams p) {
         total += q[i];
       }
       total = wave_sum(total);
+      // Times the inverse: one rounding more than a quotient per logit (half a step,
+      // 2^-24 of the gradient), for one division per token.
       const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {

@@ -27,7 +27,7 @@ def test_wide_products(dt, counts, N, K, tokens):
 @pytest.mark.parametrize("counts,N,K,tokens", [
     ([100, 0, 60], 2568, 512, None), ([100, 0, 60], 2568, 1536, 90), ([100, 0, 60], 2568, 2560, None),
     ([300, 200], 2568, 416, 77), ([300, 200], 2568, 1120, None), ([300, 200], 2568, 2880, 90),
-    ([300, 200], 2568, 2560, 77)])
+    ([300, 200], 2568, 2560, 77), ([120, 130], 4104, 1536, None), ([120, 130], 4104, 2560, 90)])
 def test_wide_4_bit_products(counts, N, K, tokens):
     check_4_bits(counts, N, K, tokens)
 
@@ -99,7 +99,7 @@ def test_rows_outside_x_are_rows_of_zeros(counts, N, K, spread, finite):
 
 
 @pytest.mark.parametrize("counts,N,K", [([100, 60], 2568, 1536), ([300, 200], 2568, 2560),
-                                        ([300, 200], 2568, 416)])
+                                        ([300, 200], 2568, 416), ([120, 130], 4104, 1536)])
 @pytest.mark.parametrize("spread", [False, True])
 @pytest.mark.parametrize("finite", [True, False])
 def test_4_bit_rows_outside_x_are_rows_of_zeros(counts, N, K, spread, finite):
