@@ -109,19 +109,20 @@ def _whole(t, name: str, shape, dtype):
 
 
 def _device(*named):
-    first = named[0]
-    dev = first.device
+    dev = named[0].device
     for t in named:
-        if t is None:
-            continue
-        if t is not first and t.device != dev:
+        if t is not None and t is not named[0] and t.device != dev:
             raise ValueError(f"operands on {dev} and {t.device}")
-        if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError("an operand requires a gradient, which no call here records: the "
-                             "gradients are calls of their own (use detach or torch.no_grad)")
     if dev.type != "cuda":
         raise ValueError(f"operands must live on a GPU, not {dev}")
     return dev
+
+
+def _recorded() -> None:
+    """For an operand that requires a gradient."""
+    if torch.is_grad_enabled():
+        raise ValueError("an operand requires a gradient, which no call here records: the "
+                         "gradients are calls of their own (use detach or torch.no_grad)")
 
 
 def _elsewhere(dev, stream) -> bool:
@@ -185,6 +186,8 @@ def route(logits, k: int, *, renormalize: bool = True, out: Routing | None = Non
     p, stride = _matrix(logits, "logits", None, _DTYPE)
     T, E = logits.shape
     need = route_workspace(T, E, k)
+    if logits.requires_grad:
+        _recorded()
     dev = _device(logits, workspace, *(out or ()))
     if _elsewhere(dev, stream):
         with _there(dev, stream):
@@ -224,6 +227,9 @@ def route_backward(logits, experts, weights, dweights, *, renormalize: bool = Tr
     p, stride = _matrix(logits, "logits", None, _DTYPE)
     T, E = logits.shape
     k = experts.shape[-1]
+    if (logits.requires_grad or weights.requires_grad or dweights.requires_grad or
+            out is not None and out.requires_grad):
+        _recorded()
     dev = _device(logits, experts, weights, dweights, out)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
@@ -254,6 +260,8 @@ def _rows_out(out, rows: int, cols: int, dtype, dev, name: str = "out"):
         out = torch.empty(rows, cols, dtype=dtype, device=dev)
         return out, out.data_ptr(), max(cols, 1)
     p, stride = _matrix(out, name, cols, (dtype,))
+    if out.requires_grad:
+        _recorded()
     if out.shape[0] != rows:
         raise ValueError(f"{name} must have {rows} rows, got {out.shape[0]}")
     return out, p, stride
@@ -273,6 +281,8 @@ def gmm(x, w, counts, *, index=None, out=None, status=None, check: bool = False,
     wp = _whole(w, "w", (E, N, K), x.dtype)
     rows = x.shape[0] if index is None else index.numel()
     cp, ip = _grouped(counts, index, E, rows)
+    if x.requires_grad or w.requires_grad or out is not None and out.requires_grad:
+        _recorded()
     dev = _device(x, w, counts, index, out, status)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
@@ -296,6 +306,8 @@ def gmm_dx(dy, w, counts, *, out=None, status=None, check: bool = False, stream=
         raise ValueError(f"dy must have {N} columns, got {dy.shape[1]}")
     wp = _whole(w, "w", (E, N, K), dy.dtype)
     cp, _ = _grouped(counts, None, E, rows)
+    if dy.requires_grad or w.requires_grad or out is not None and out.requires_grad:
+        _recorded()
     dev = _device(dy, w, counts, out, status)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
@@ -318,6 +330,8 @@ def gmm_dw(dy, x, counts, *, index=None, out=None, out_dtype=None, status=None,
     cp, ip = _grouped(counts, index, E, rows)
     if out_dtype is None:
         out_dtype = dy.dtype if out is None else out.dtype
+    if dy.requires_grad or x.requires_grad or out is not None and out.requires_grad:
+        _recorded()
     dev = _device(dy, x, counts, index, out, status)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
@@ -348,6 +362,9 @@ def combine(y, place, weights=None, *, out=None, status=None, check: bool = Fals
     out, without ``weights`` each counts once."""
     yp, ys = _matrix(y, "y", None, _DTYPE)
     T, k, pp, wp = _slots(place, weights)
+    if (y.requires_grad or weights is not None and weights.requires_grad or
+            out is not None and out.requires_grad):
+        _recorded()
     dev = _device(y, place, weights, out, status)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
@@ -370,6 +387,9 @@ def combine_backward(dout, y, place, weights=None, *, out=None, status=None, che
     T, k, pp, wp = _slots(place, weights)
     if dout.shape[0] != T:
         raise ValueError(f"dout must have {T} rows, got {dout.shape[0]}")
+    if (dout.requires_grad or y.requires_grad or
+            weights is not None and weights.requires_grad):
+        _recorded()
     dev = _device(dout, y, place, weights, status, *(out or ()))
     if _elsewhere(dev, stream):
         with _there(dev, stream):
@@ -396,6 +416,8 @@ def mx4_quantize(x, *, out=None, stream=None):
     p, stride = _matrix(x, "x", None, _DTYPE)
     rows, cols = x.shape
     B = (cols + 31) // 32
+    if x.requires_grad:
+        _recorded()
     dev = _device(x, *(out or ()))
     if _elsewhere(dev, stream):
         with _there(dev, stream):
