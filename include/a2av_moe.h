@@ -44,7 +44,8 @@ extern "C" {
  * fewer than k other logits has empty slots.  With p = softmax(logits[t]):
  *   experts[t][j]  the j-th expert, -1 for an empty slot
  *   weights[t][j]  p of that expert, with renormalize != 0 divided by the sum
- *                  over the token's chosen ones; 0 for an empty slot
+ *                  over the token's chosen ones; 0 for an empty slot, and where
+ *                  exp(l - largest l) lies below 2^-126
  *   counts[e]      tokens that chose e
  *   order[r]       the token of row r when the slots stand in expert order,
  *                  within an expert by token: the gather list that the
@@ -97,7 +98,8 @@ int a2av_moe_route_backward(const void *logits, int64_t logits_stride, int64_t t
  * dtype FP16 or BF16 for every operand; dw_dtype is dtype or FP32.  An expert
  * without rows gets dW = 0.
  * Device checks: a negative count, or counts that sum to more than `rows` ->
- * INVALID_ARGS, nothing written; an index in use outside [0, x_rows) ->
+ * INVALID_ARGS, nothing written (a forward product or gmm_dx of 0 rows enqueues
+ * nothing and looks at no counts); an index in use outside [0, x_rows) ->
  * INVALID_ARGS, and that row counts as a row of zeros: its y is 0, or NaN where
  * W holds a NaN or an infinity (in dW, where dy does).
  * Limits: rows, x_rows, N, K <= 2^30, E in 1..4096.
