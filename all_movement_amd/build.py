@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liba2av.so")
 SOURCES = ["runtime.hip", "kernels.hip", "plan.cpp", "probe.hip", "moe_host.hip", "moe_gemm.hip",
-           "moe_route.hip", "moe_rows.hip"]
+           "moe_fp8.hip", "moe_route.hip", "moe_rows.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

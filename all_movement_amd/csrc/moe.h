@@ -30,7 +30,7 @@ struct GmmParams {
   int64_t nrows;           // grouped rows
   int32_t E;
   int32_t N, K;            // of the weights
-  int32_t blocks;          // MX4: scale blocks of a row
+  int32_t blocks;          // scale blocks of a row (MX4), of a weight's row (8 bits)
   int32_t out_type;        // a2av_dtype of out
 };
 
@@ -82,13 +82,29 @@ struct Mx4Params {
   int32_t rows, cols, blocks, dtype;
 };
 
+// 8-bit rows (n = 0), or weights [rows / n, n, cols].
+struct Fp8Params {
+  const void* x;
+  void* out;
+  const uint8_t* codes_in;
+  const uint8_t* scales_in;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t stride;          // elements, of x or out
+  int64_t rows;
+  int32_t n, cols, blocks, dtype;
+};
+
 hipError_t launch_gmm(const GmmParams& p, GmmType type, GmmMode mode, hipStream_t stream);
+hipError_t launch_gmm_fp8(const GmmParams& p, GmmMode mode, hipStream_t stream);
 hipError_t launch_route(RouteParams p, hipStream_t stream);
 hipError_t launch_route_back(const RouteBackParams& p, hipStream_t stream);
 hipError_t launch_combine(const CombineParams& p, hipStream_t stream);
 hipError_t launch_combine_back(const CombineParams& p, hipStream_t stream);
 hipError_t launch_mx4_quantize(const Mx4Params& p, hipStream_t stream);
 hipError_t launch_mx4_dequantize(const Mx4Params& p, hipStream_t stream);
+hipError_t launch_fp8_quantize(const Fp8Params& p, hipStream_t stream);
+hipError_t launch_fp8_dequantize(const Fp8Params& p, hipStream_t stream);
 
 // The router's blocks: tokens of one workgroup of its first kernel, 8 to 64, so
 // that there are 256 blocks (one per CU) as soon as there are tokens for it.

@@ -1,5 +1,5 @@
 // moe_host.hip -- the entry points of include/a2av_moe.h: host checks, then
-// the launches of moe_gemm.hip, moe_route.hip and moe_rows.hip.  No device
+// the launches of moe_gemm.hip, moe_fp8.hip, moe_route.hip and moe_rows.hip.  No device
 // code, no state: what an operator needs comes with the call.
 #include <hip/hip_runtime.h>
 
@@ -137,6 +137,110 @@ bool bad_gmm_sizes(int64_t x_rows, int64_t rows, int32_t E, int64_t N, int64_t K
 int check_route_sizes(int64_t tokens, int32_t E, int32_t k) {
   if (tokens < 0 || E < 1 || E > 1024 || k < 1 || k > 16 || k > E) return A2AV_ERR_INVALID_ARGS;
   return tokens > kMostSize / k ? A2AV_ERR_INVALID_ARGS : A2AV_OK;
+}
+
+// Blocks of 128 of a row of 8-bit values, and the scale bytes of such a row.
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+int64_t fp8_pitch(int64_t n) { return (blocks128(n) + 3) / 4 * 4; }
+
+int fp8_rows(const void* x, int64_t x_stride, int64_t rows, int64_t cols, int32_t dtype,
+             const uint8_t* codes, const uint8_t* scales, bool quantize, hipStream_t stream) {
+  const bool sizes_bad = bad_size(rows, 0) || bad_size(cols, 1) || x_stride < cols ||
+                         x_stride > kMax31;
+  const std::initializer_list<Operand> all = {
+      matrix(x, sizes_bad, rows, x_stride, cols, size_of(dtype), !quantize),
+      {codes, sizes_bad ? 1 : rows * blocks128(cols) * 128, quantize, 16},
+      {scales, sizes_bad ? 1 : rows * fp8_pitch(cols), quantize, 4}};
+  if (any_null(all)) return A2AV_ERR_NULLPTR;
+  if (!is_float(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
+  if (sizes_bad || bad_addresses(all)) return A2AV_ERR_INVALID_ARGS;
+  if (rows == 0) return A2AV_OK;
+  Fp8Params p{};
+  p.x = x;
+  p.out = const_cast<void*>(x);
+  p.codes = const_cast<uint8_t*>(codes);
+  p.scales = const_cast<uint8_t*>(scales);
+  p.codes_in = codes;
+  p.scales_in = scales;
+  p.stride = x_stride;
+  p.rows = rows;
+  p.cols = int32_t(cols);
+  p.blocks = int32_t(blocks128(cols));
+  p.dtype = dtype;
+  return launched(quantize ? launch_fp8_quantize(p, stream) : launch_fp8_dequantize(p, stream));
+}
+
+int fp8_weights(const void* w, int32_t E, int64_t N, int64_t K, int32_t dtype, const uint8_t* codes,
+                const uint8_t* scales, bool quantize, hipStream_t stream) {
+  const bool sizes_bad = E < 1 || E > 4096 || bad_size(N, 1) || bad_size(K, 1) ||
+                         N * K > (int64_t(1) << 58) / E;
+  const int64_t z = size_of(dtype);
+  const std::initializer_list<Operand> all = {
+      {w, sizes_bad ? 1 : E * N * K * z, !quantize, z},
+      {codes, sizes_bad ? 1 : E * N * blocks128(K) * 128, quantize, 16},
+      {scales, sizes_bad ? 1 : E * blocks128(N) * fp8_pitch(K), quantize, 4}};
+  if (any_null(all)) return A2AV_ERR_NULLPTR;
+  if (!is_float(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
+  if (sizes_bad || bad_addresses(all)) return A2AV_ERR_INVALID_ARGS;
+  Fp8Params p{};
+  p.x = w;
+  p.out = const_cast<void*>(w);
+  p.codes = const_cast<uint8_t*>(codes);
+  p.scales = const_cast<uint8_t*>(scales);
+  p.codes_in = codes;
+  p.scales_in = scales;
+  p.stride = K;
+  p.rows = E * N;
+  p.n = int32_t(N);
+  p.cols = int32_t(K);
+  p.blocks = int32_t(blocks128(K));
+  p.dtype = dtype;
+  return launched(quantize ? launch_fp8_quantize(p, stream) : launch_fp8_dequantize(p, stream));
+}
+
+// The 8-bit products: rows of x (forward) or dy, of `red` values each, give rows
+// of `out` values.
+int gmm_fp8(GmmMode mode, const uint8_t* x_codes, const uint8_t* x_scales, int64_t x_rows,
+            const uint8_t* w_codes, const uint8_t* w_scales, const int32_t* counts,
+            const int32_t* index, void* y, int64_t y_stride, int64_t rows, int32_t E, int64_t N,
+            int64_t K, int32_t y_dtype, int32_t* status, hipStream_t stream) {
+  const int64_t out = mode == kGmmFwd ? N : K, red = mode == kGmmFwd ? K : N;
+  const bool sizes_bad = bad_gmm_sizes(x_rows, rows, E, N, K, index) || y_stride < out ||
+                         y_stride > kMax31;
+  const bool some = sizes_bad || rows > 0;
+  const std::initializer_list<Operand> all = {
+      {x_codes, sizes_bad ? 1 : x_rows * blocks128(red) * 128, false, 16},
+      {x_scales, sizes_bad ? 1 : x_rows * fp8_pitch(red), false, 4},
+      {w_codes, sizes_bad ? 1 : E * N * blocks128(K) * 128, false, 16},
+      {w_scales, sizes_bad ? 1 : E * blocks128(N) * fp8_pitch(K), false, 4},
+      {counts, sizes_bad ? 1 : int64_t(E) * 4, false, 4},
+      {index, sizes_bad ? 1 : rows * 4, false, 4, true},
+      matrix(y, sizes_bad, rows, y_stride, out, size_of(y_dtype), true),
+      {status, 4, true, 4, true}};
+  if (some && any_null(all)) return A2AV_ERR_NULLPTR;
+  if (!is_float(y_dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
+  if (sizes_bad || bad_addresses(all)) return A2AV_ERR_INVALID_ARGS;
+  if (rows == 0) return A2AV_OK;
+  GmmParams p{};
+  p.rows = x_codes;
+  p.other = w_codes;
+  p.row_scales = x_scales;
+  p.other_scales = w_scales;
+  p.out = static_cast<uint8_t*>(y);
+  p.counts = counts;
+  p.index = index;
+  p.status = status;
+  p.row_stride = blocks128(red) * 128;
+  p.other_stride = blocks128(K) * 128;
+  p.out_stride = y_stride;
+  p.x_rows = x_rows;
+  p.nrows = rows;
+  p.E = E;
+  p.N = int32_t(N);
+  p.K = int32_t(K);
+  p.blocks = int32_t(blocks128(K));
+  p.out_type = y_dtype;
+  return launched(launch_gmm_fp8(p, mode, stream));
 }
 
 }  // namespace
@@ -495,6 +599,44 @@ int a2av_moe_gmm_mx4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t x_
   p.blocks = int32_t(blocks);
   p.out_type = y_dtype;
   return launched(launch_gmm(p, kGmmMX4, kGmmFwd, static_cast<hipStream_t>(stream)));
+}
+
+int a2av_moe_fp8_quantize(const void* x, int64_t x_stride, int64_t rows, int64_t cols,
+                          int32_t dtype, uint8_t* codes, uint8_t* scales, void* stream) {
+  return fp8_rows(x, x_stride, rows, cols, dtype, codes, scales, true,
+                  static_cast<hipStream_t>(stream));
+}
+
+int a2av_moe_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                            int32_t dtype, void* x, int64_t x_stride, void* stream) {
+  return fp8_rows(x, x_stride, rows, cols, dtype, codes, scales, false,
+                  static_cast<hipStream_t>(stream));
+}
+
+int a2av_moe_fp8_quantize_weights(const void* w, int32_t E, int64_t N, int64_t K, int32_t dtype,
+                                  uint8_t* codes, uint8_t* scales, void* stream) {
+  return fp8_weights(w, E, N, K, dtype, codes, scales, true, static_cast<hipStream_t>(stream));
+}
+
+int a2av_moe_fp8_dequantize_weights(const uint8_t* codes, const uint8_t* scales, int32_t E,
+                                    int64_t N, int64_t K, int32_t dtype, void* w, void* stream) {
+  return fp8_weights(w, E, N, K, dtype, codes, scales, false, static_cast<hipStream_t>(stream));
+}
+
+int a2av_moe_gmm_fp8(const uint8_t* x_codes, const uint8_t* x_scales, int64_t x_rows,
+                     const uint8_t* w_codes, const uint8_t* w_scales, const int32_t* counts,
+                     const int32_t* index, void* y, int64_t y_stride, int64_t rows, int32_t E,
+                     int64_t N, int64_t K, int32_t y_dtype, int32_t* status, void* stream) {
+  return gmm_fp8(kGmmFwd, x_codes, x_scales, x_rows, w_codes, w_scales, counts, index, y, y_stride,
+                 rows, E, N, K, y_dtype, status, static_cast<hipStream_t>(stream));
+}
+
+int a2av_moe_gmm_fp8_dx(const uint8_t* dy_codes, const uint8_t* dy_scales, const uint8_t* w_codes,
+                        const uint8_t* w_scales, const int32_t* counts, void* dx, int64_t dx_stride,
+                        int64_t rows, int32_t E, int64_t N, int64_t K, int32_t dx_dtype,
+                        int32_t* status, void* stream) {
+  return gmm_fp8(kGmmDx, dy_codes, dy_scales, rows, w_codes, w_scales, counts, nullptr, dx,
+                 dx_stride, rows, E, N, K, dx_dtype, status, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
 // moe_rows.hip -- the weighted return of rows to their tokens, its gradients,
-// and the 4-bit format of rows.  All of it is bound by memory: each kernel
+// and the 4-bit and 8-bit formats of rows and weights.  All of it is bound by memory: each kernel
 // reads and writes every row once, 16 bytes per lane where the rows' alignment
 // allows it.
 #include <hip/hip_runtime.h>
@@ -306,6 +306,186 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const Mx4Params p) {
   }
 }
 
+// ------------------------------------------------------------------ 8-bit rows and weights
+
+// The scale byte of a block from the bits of its largest magnitude: the least s
+// with 448 * 2^(s - 127) at or above it.  448 is 1.75 * 2^8: a mantissa past
+// 1.75, 0x600000, carries into the exponent.
+__device__ inline int fp8_scale(uint32_t top) {
+  if (top >= 0x7f800000u) return 255;
+  const int s = int((top + 0x1fffffu) >> 23) - 8;
+  return s > 0 ? s : 0;
+}
+
+// 4 codes; the products with 2^(127 - s) are exact, so that each value is
+// rounded once.
+__device__ inline uint32_t fp8_codes(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+}
+
+// 8 values of a row of `cols` from column `col` on, zeros past its end.
+template <int DT, bool WHOLE>
+__device__ inline void load_eight(const typename Elem<DT>::type* x, int col, int cols,
+                                  float (&v)[8]) {
+  if constexpr (WHOLE && DT == A2AV_FP32) {
+    const auto lo = load_n<DT, 4, true>(x), hi = load_n<DT, 4, true>(x + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[i + 4] = hi[i];
+  } else if (WHOLE || col + 8 <= cols) {
+    const auto w = load_n<DT, 8, WHOLE>(x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? Elem<DT>::up(x[i]) : 0.0f;
+  }
+}
+
+__device__ inline uint32_t top_of(const float (&v)[8]) {
+  uint32_t top = 0;  // magnitudes order like their bits
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = __float_as_uint(v[i]) & 0x7fffffffu;
+    top = m > top ? m : top;
+  }
+  return top;
+}
+
+__device__ inline uint2 eight_codes(const float (&v)[8], int s) {
+  if (s == 255) return uint2{0, 0};
+  const float up = __uint_as_float(uint32_t(254 - s) << 23);
+  return uint2{fp8_codes(v[0] * up, v[1] * up, v[2] * up, v[3] * up),
+               fp8_codes(v[4] * up, v[5] * up, v[6] * up, v[7] * up)};
+}
+
+// Sixteen lanes per block of 128, 8 values each.
+template <int DT, bool WHOLE>
+__global__ __launch_bounds__(256) void fp8_rows_kernel(const Fp8Params p) {
+  using T = typename Elem<DT>::type;
+  const int64_t all = p.rows * p.blocks * 16;
+  const int pitch = (p.blocks + 3) / 4 * 4;
+  for (int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x; q < all;
+       q += int64_t(gridDim.x) * 256) {
+    const int64_t block = q >> 4, row = block / p.blocks;
+    const int b = int(block - row * p.blocks);
+    const int col = b * 128 + int(q & 15) * 8;
+    float v[8];
+    load_eight<DT, WHOLE>(static_cast<const T*>(p.x) + row * p.stride + col, col, p.cols, v);
+    uint32_t top = top_of(v);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) {
+      const uint32_t u = __shfl_xor(top, d);
+      top = u > top ? u : top;
+    }
+    const int s = fp8_scale(top);
+    reinterpret_cast<uint2*>(p.codes)[q] = eight_codes(v, s);
+    if ((q & 15) == 0) {
+      uint8_t* to = p.scales + row * pitch;
+      to[b] = uint8_t(s);
+      if (b == p.blocks - 1)
+        for (int i = p.blocks; i < pitch; ++i) to[i] = 0;
+    }
+  }
+}
+
+// A workgroup per 128 x 128 block of a weight, 16 rows at a time.
+template <int DT, bool WHOLE>
+__global__ __launch_bounds__(256) void fp8_weights_kernel(const Fp8Params p) {
+  using T = typename Elem<DT>::type;
+  __shared__ uint32_t tops[4];
+  const int tid = threadIdx.x, pitch = (p.blocks + 3) / 4 * 4;
+  const int tall = (p.n + 127) / 128;
+  const int64_t all = p.rows / p.n * tall * p.blocks;
+  for (int64_t block = blockIdx.x; block < all; block += gridDim.x) {
+    const int64_t strip = block / p.blocks, e = strip / tall;
+    const int b = int(block - strip * p.blocks);
+    const int n0 = int(strip - e * tall) * 128;
+    const int col = b * 128 + (tid & 15) * 8;
+    float v[8][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = n0 + i * 16 + (tid >> 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+      if (n < p.n) {
+        const T* x = static_cast<const T*>(p.x) + (e * p.n + n) * p.stride + col;
+        load_eight<DT, WHOLE>(x, col, p.cols, v[i]);
+      }
+      const uint32_t u = top_of(v[i]);
+      top = u > top ? u : top;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t u = __shfl_xor(top, d);
+      top = u > top ? u : top;
+    }
+    if ((tid & 63) == 0) tops[tid >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = tops[i] > top ? tops[i] : top;
+    __syncthreads();
+    const int s = fp8_scale(top);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = n0 + i * 16 + (tid >> 4);
+      if (n < p.n)
+        reinterpret_cast<uint2*>(p.codes)[(e * p.n + n) * (p.blocks * 16) + b * 16 + (tid & 15)] =
+            eight_codes(v[i], s);
+    }
+    if (tid == 0) {
+      uint8_t* to = p.scales + strip * pitch;
+      to[b] = uint8_t(s);
+      if (b == p.blocks - 1)
+        for (int i = p.blocks; i < pitch; ++i) to[i] = 0;
+    }
+  }
+}
+
+template <int DT, bool WHOLE>
+__global__ __launch_bounds__(256) void fp8_values_kernel(const Fp8Params p) {
+  using T = typename Elem<DT>::type;
+  const int64_t all = p.rows * p.blocks * 16;
+  const int pitch = (p.blocks + 3) / 4 * 4;
+  for (int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x; q < all;
+       q += int64_t(gridDim.x) * 256) {
+    const int64_t block = q >> 4, row = block / p.blocks;
+    const int b = int(block - row * p.blocks);
+    const int col = b * 128 + int(q & 15) * 8;
+    int64_t strip = row;
+    if (p.n) {
+      const int64_t e = row / p.n;
+      strip = e * ((p.n + 127) / 128) + (row - e * p.n) / 128;
+    }
+    const uint2 codes = reinterpret_cast<const uint2*>(p.codes_in)[q];
+    const uint32_t s = p.scales_in[strip * pitch + b];
+    // 2^(s - 127); below the normal numbers for s = 0, NaN for s = 255.
+    const float step = __uint_as_float(s == 255 ? 0x7fc00000u : s ? s << 23 : 0x00400000u);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const int w = int(i ? codes.y : codes.x);
+      v[i] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * step;
+      v[i + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * step;
+      v[i + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * step;
+      v[i + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * step;
+    }
+    T* x = static_cast<T*>(p.out) + row * p.stride + col;
+    if constexpr (WHOLE && DT == A2AV_FP32) {
+      const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+      store_n<DT, 4, true, true>(x, lo);
+      store_n<DT, 4, true, true>(x + 4, hi);
+    } else if (WHOLE || col + 8 <= p.cols) {
+      store_n<DT, 8, WHOLE, true>(x, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (col + i < p.cols) x[i] = Elem<DT>::down(v[i]);
+    }
+  }
+}
+
 template <class F>
 hipError_t with_dtype(int dtype, F f) {
   (void)hipGetLastError();
@@ -408,6 +588,43 @@ hipError_t launch_mx4_dequantize(const Mx4Params& p, hipStream_t stream) {
       dequantize_kernel<DT, true><<<grid, dim3(256), 0, stream>>>(p);
     else
       dequantize_kernel<DT, false><<<grid, dim3(256), 0, stream>>>(p);
+  });
+}
+
+// Whether rows of x or out are whole blocks of aligned pieces.
+static bool whole_rows(const Fp8Params& p, const void* rows) {
+  return p.cols % 128 == 0 && p.stride % (16 / size_of(p.dtype)) == 0 &&
+         reinterpret_cast<uintptr_t>(rows) % 16 == 0;
+}
+
+hipError_t launch_fp8_quantize(const Fp8Params& p, hipStream_t stream) {
+  const bool whole = whole_rows(p, p.x);
+  const int64_t want = p.n ? p.rows / p.n * ((p.n + 127) / 128) * p.blocks
+                           : (p.rows * p.blocks * 16 + 255) / 256;
+  const dim3 grid(uint32_t(want < (1 << 20) ? want : (1 << 20)));
+  return with_dtype(p.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (p.n && whole)
+      fp8_weights_kernel<DT, true><<<grid, dim3(256), 0, stream>>>(p);
+    else if (p.n)
+      fp8_weights_kernel<DT, false><<<grid, dim3(256), 0, stream>>>(p);
+    else if (whole)
+      fp8_rows_kernel<DT, true><<<grid, dim3(256), 0, stream>>>(p);
+    else
+      fp8_rows_kernel<DT, false><<<grid, dim3(256), 0, stream>>>(p);
+  });
+}
+
+hipError_t launch_fp8_dequantize(const Fp8Params& p, hipStream_t stream) {
+  const bool whole = whole_rows(p, p.out);
+  const int64_t want = (p.rows * p.blocks * 16 + 255) / 256;
+  const dim3 grid(uint32_t(want < (1 << 20) ? want : (1 << 20)));
+  return with_dtype(p.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (whole)
+      fp8_values_kernel<DT, true><<<grid, dim3(256), 0, stream>>>(p);
+    else
+      fp8_values_kernel<DT, false><<<grid, dim3(256), 0, stream>>>(p);
   });
 }
 

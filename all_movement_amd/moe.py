@@ -4,7 +4,9 @@
 that the exchange and the products take; ``gmm``, ``gmm_dx`` and ``gmm_dw`` are
 the products grouped by expert and their gradients; ``combine`` returns the
 rows to their tokens; ``mx4_quantize``, ``mx4_dequantize`` and ``gmm_mx4`` are
-the microscaled 4-bit format and the product on it.
+the microscaled 4-bit format and the product on it; ``fp8_quantize``,
+``fp8_quantize_weights``, their inverses, ``gmm_fp8`` and ``gmm_fp8_dx`` are the
+8-bit format and the products on it.
 
 Every step runs in the HIP library.  Nothing is converted or copied: a tensor
 that would need it is refused.  Rows may be strided, everything else is
@@ -35,7 +37,9 @@ from . import a2av
 MOE_EXPORTS = ["a2av_moe_route_workspace", "a2av_moe_route", "a2av_moe_route_backward",
                "a2av_moe_gmm", "a2av_moe_gmm_dx", "a2av_moe_gmm_dw", "a2av_moe_combine",
                "a2av_moe_combine_backward", "a2av_moe_mx4_quantize", "a2av_moe_mx4_dequantize",
-               "a2av_moe_gmm_mx4"]
+               "a2av_moe_gmm_mx4", "a2av_moe_fp8_quantize", "a2av_moe_fp8_dequantize",
+               "a2av_moe_fp8_quantize_weights", "a2av_moe_fp8_dequantize_weights",
+               "a2av_moe_gmm_fp8", "a2av_moe_gmm_fp8_dx"]
 
 _DTYPE = {torch.float32: a2av.FP32, torch.float16: a2av.FP16, torch.bfloat16: a2av.BF16}
 _lib = None
@@ -63,6 +67,13 @@ def lib() -> ctypes.CDLL:
         "a2av_moe_mx4_dequantize": [vp, vp, i64, i64, i32, vp, i64, vp],
         "a2av_moe_gmm_mx4": [vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i32, i64, i64, i32, vp,
                              vp],
+        "a2av_moe_fp8_quantize": [vp, i64, i64, i64, i32, vp, vp, vp],
+        "a2av_moe_fp8_dequantize": [vp, vp, i64, i64, i32, vp, i64, vp],
+        "a2av_moe_fp8_quantize_weights": [vp, i32, i64, i64, i32, vp, vp, vp],
+        "a2av_moe_fp8_dequantize_weights": [vp, vp, i32, i64, i64, i32, vp, vp],
+        "a2av_moe_gmm_fp8": [vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i32, i64, i64, i32, vp,
+                             vp],
+        "a2av_moe_gmm_fp8_dx": [vp, vp, vp, vp, vp, vp, i64, i64, i32, i64, i64, i32, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -474,4 +485,171 @@ def gmm_mx4(x_codes, x_scales, w_codes, w_scales, counts, *, index=None, dtype=t
     st = lib().a2av_moe_gmm_mx4(*ptr, cp, ip, op, os, rows, E, N, B * 32, _DTYPE.get(dtype, -1),
                                 sp, _stream(dev))
     _done(st, "a2av_moe_gmm_mx4", status, check)
+    return out
+
+
+# ---------------------------------------------------------------- 8-bit rows and weights
+
+E4M3 = torch.float8_e4m3fn
+
+
+def _blocks(n: int):
+    """(code bytes, scale bytes) of a row of n 8-bit values."""
+    B = (n + 127) // 128
+    return B * 128, (B + 3) // 4 * 4
+
+
+def fp8_quantize(x, *, out=None, stream=None):
+    """(codes float8_e4m3fn [rows, 128 * B], scales uint8 [rows, 4 * ceil(B / 4)]) of x
+    [rows, cols], with B = ceil(cols / 128) blocks to a row."""
+    p, stride = _matrix(x, "x", None, _DTYPE)
+    rows, cols = x.shape
+    C, S = _blocks(cols)
+    if x.requires_grad or out is not None and out[0].requires_grad:
+        _recorded()
+    dev = _device(x, *(out or ()))
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return fp8_quantize(x, out=out)
+    if out is None:
+        out = (torch.empty(rows, C, dtype=E4M3, device=dev),
+               torch.empty(rows, S, dtype=torch.uint8, device=dev))
+    st = lib().a2av_moe_fp8_quantize(p, stride, rows, cols, _DTYPE[x.dtype],
+                                     _whole(out[0], "codes", (rows, C), E4M3),
+                                     _whole(out[1], "scales", (rows, S), torch.uint8),
+                                     _stream(dev))
+    a2av._raise(st, "a2av_moe_fp8_quantize")
+    return out
+
+
+def fp8_dequantize(codes, scales, cols: int, dtype=torch.bfloat16, *, out=None, stream=None):
+    """The values [rows, cols] of :func:`fp8_quantize`'s codes and scales."""
+    rows = scales.shape[0]
+    C, S = _blocks(cols)
+    cp = _whole(codes, "codes", (rows, C), E4M3)
+    sp = _whole(scales, "scales", (rows, S), torch.uint8)
+    if codes.requires_grad:
+        _recorded()
+    dev = _device(codes, scales, out)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return fp8_dequantize(codes, scales, cols, dtype, out=out)
+    out, op, os = _rows_out(out, rows, cols, dtype, dev)
+    st = lib().a2av_moe_fp8_dequantize(cp, sp, rows, cols, _DTYPE.get(dtype, -1), op, os,
+                                       _stream(dev))
+    a2av._raise(st, "a2av_moe_fp8_dequantize")
+    return out
+
+
+def fp8_quantize_weights(w, *, out=None, stream=None):
+    """(codes float8_e4m3fn [E, N, 128 * B], scales uint8 [E, ceil(N / 128), 4 * ceil(B / 4)])
+    of w [E, N, K], with B = ceil(K / 128): a scale for each 128 x 128 block."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch tensor")
+    if w.dim() != 3:
+        raise ValueError(f"w must be [experts, N, K], got {tuple(w.shape)}")
+    if w.dtype not in _DTYPE:
+        raise ValueError(f"w must be one of {tuple(_DTYPE)}, got {w.dtype}")
+    E, N, K = w.shape
+    wp = _whole(w, "w", (E, N, K), w.dtype)
+    C, S = _blocks(K)
+    if w.requires_grad or out is not None and out[0].requires_grad:
+        _recorded()
+    dev = _device(w, *(out or ()))
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return fp8_quantize_weights(w, out=out)
+    strips = (N + 127) // 128
+    if out is None:
+        out = (torch.empty(E, N, C, dtype=E4M3, device=dev),
+               torch.empty(E, strips, S, dtype=torch.uint8, device=dev))
+    st = lib().a2av_moe_fp8_quantize_weights(wp, E, N, K, _DTYPE[w.dtype],
+                                             _whole(out[0], "codes", (E, N, C), E4M3),
+                                             _whole(out[1], "scales", (E, strips, S), torch.uint8),
+                                             _stream(dev))
+    a2av._raise(st, "a2av_moe_fp8_quantize_weights")
+    return out
+
+
+def _fp8_weight(codes, scales, cols: int | None):
+    """(codes' pointer, scales' pointer, E, N, K) of a weight of ``cols`` columns
+    (None: as many as there are codes)."""
+    if codes.dim() != 3:
+        raise ValueError(f"w_codes must be [experts, N, 128 * B], got {tuple(codes.shape)}")
+    E, N, K = codes.shape
+    if cols is not None:
+        K = cols
+    C, S = _blocks(K)
+    return (_whole(codes, "w_codes", (E, N, C), E4M3),
+            _whole(scales, "w_scales", (E, (N + 127) // 128, S), torch.uint8), E, N, K)
+
+
+def fp8_dequantize_weights(codes, scales, cols: int, dtype=torch.bfloat16, *, out=None,
+                           stream=None):
+    """The values [E, N, cols] of :func:`fp8_quantize_weights`'s codes and scales."""
+    cp, sp, E, N, K = _fp8_weight(codes, scales, cols)
+    if codes.requires_grad or out is not None and out.requires_grad:
+        _recorded()
+    dev = _device(codes, scales, out)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return fp8_dequantize_weights(codes, scales, cols, dtype, out=out)
+    if out is None:
+        out = torch.empty(E, N, K, dtype=dtype, device=dev)
+    st = lib().a2av_moe_fp8_dequantize_weights(cp, sp, E, N, K, _DTYPE.get(dtype, -1),
+                                               _whole(out, "out", (E, N, K), dtype), _stream(dev))
+    a2av._raise(st, "a2av_moe_fp8_dequantize_weights")
+    return out
+
+
+def gmm_fp8(x_codes, x_scales, w_codes, w_scales, counts, *, index=None, dtype=torch.bfloat16,
+            out=None, status=None, check: bool = False, stream=None):
+    """:func:`gmm` on 8-bit rows and weights: ``x_codes`` and ``x_scales`` of
+    :func:`fp8_quantize`, ``w_codes`` and ``w_scales`` of :func:`fp8_quantize_weights`;
+    y in ``dtype``."""
+    wc, ws, E, N, K = _fp8_weight(w_codes, w_scales, None)
+    C, S = _blocks(K)
+    x_rows = x_codes.shape[0]
+    xc = _whole(x_codes, "x_codes", (x_rows, C), E4M3)
+    xs = _whole(x_scales, "x_scales", (x_rows, S), torch.uint8)
+    rows = x_rows if index is None else index.numel()
+    cp, ip = _grouped(counts, index, E, rows)
+    if x_codes.requires_grad or w_codes.requires_grad:
+        _recorded()
+    dev = _device(x_codes, x_scales, w_codes, w_scales, counts, index, out, status)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gmm_fp8(x_codes, x_scales, w_codes, w_scales, counts, index=index, dtype=dtype,
+                           out=out, status=status, check=check)
+    out, op, os = _rows_out(out, rows, N, dtype, dev)
+    status, sp = _status(status, check, dev)
+    st = lib().a2av_moe_gmm_fp8(xc, xs, x_rows, wc, ws, cp, ip, op, os, rows, E, N, K,
+                                _DTYPE.get(dtype, -1), sp, _stream(dev))
+    _done(st, "a2av_moe_gmm_fp8", status, check)
+    return out
+
+
+def gmm_fp8_dx(dy_codes, dy_scales, w_codes, w_scales, counts, *, cols: int | None = None,
+               dtype=torch.bfloat16, out=None, status=None, check: bool = False, stream=None):
+    """:func:`gmm_dx` on 8-bit rows and weights: ``dy_codes`` and ``dy_scales`` of
+    :func:`fp8_quantize` on dy [rows, N]; ``cols`` is K, the weight's columns (default:
+    as many as it has codes in a row); dx in ``dtype``."""
+    wc, ws, E, N, K = _fp8_weight(w_codes, w_scales, cols)
+    C, S = _blocks(N)
+    rows = dy_codes.shape[0]
+    yc = _whole(dy_codes, "dy_codes", (rows, C), E4M3)
+    ys = _whole(dy_scales, "dy_scales", (rows, S), torch.uint8)
+    cp, _ = _grouped(counts, None, E, rows)
+    if dy_codes.requires_grad or w_codes.requires_grad:
+        _recorded()
+    dev = _device(dy_codes, dy_scales, w_codes, w_scales, counts, out, status)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gmm_fp8_dx(dy_codes, dy_scales, w_codes, w_scales, counts, cols=cols,
+                              dtype=dtype, out=out, status=status, check=check)
+    out, op, os = _rows_out(out, rows, K, dtype, dev)
+    status, sp = _status(status, check, dev)
+    st = lib().a2av_moe_gmm_fp8_dx(yc, ys, wc, ws, cp, op, os, rows, E, N, K,
+                                   _DTYPE.get(dtype, -1), sp, _stream(dev))
+    _done(st, "a2av_moe_gmm_fp8_dx", status, check)
     return out
