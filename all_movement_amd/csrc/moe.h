@@ -45,6 +45,10 @@ struct RouteParams {
   int32_t* place;
   int32_t* hist;           // workspace [E][blocks]
   int32_t per_block;       // tokens of a block (set by launch_route)
+  // The router by groups: groups > 0.
+  int32_t groups, top_groups, group_best, sigmoid;
+  const float* bias;       // may be null
+  float scale;
 };
 
 struct RouteBackParams {
@@ -55,6 +59,8 @@ struct RouteBackParams {
   const float* weights;
   const float* dweights;
   void* dlogits;
+  int32_t grouped, sigmoid;
+  float scale;
 };
 
 struct CombineParams {

@@ -139,6 +139,17 @@ int check_route_sizes(int64_t tokens, int32_t E, int32_t k) {
   return tokens > kMostSize / k ? A2AV_ERR_INVALID_ARGS : A2AV_OK;
 }
 
+bool bad_groups(int32_t E, int32_t k, int32_t groups, int32_t top_groups, int32_t group_best) {
+  return groups < 1 || groups > 64 || E % groups || top_groups < 1 || top_groups > groups ||
+         k > top_groups * (E / groups) || group_best < 1 || group_best > 2;
+}
+
+// The scale is a positive number that has an inverse.
+bool bad_scores(int32_t scores, float scale) {
+  return (scores != A2AV_MOE_SOFTMAX && scores != A2AV_MOE_SIGMOID) ||
+         !(scale >= 0x1p-100f && scale <= 0x1p100f);
+}
+
 // Blocks of 128 of a row of 8-bit values, and the scale bytes of such a row.
 int64_t blocks128(int64_t n) { return (n + 127) / 128; }
 int64_t fp8_pitch(int64_t n) { return (blocks128(n) + 3) / 4 * 4; }
@@ -319,6 +330,88 @@ int a2av_moe_route_backward(const void* logits, int64_t logits_stride, int64_t t
   p.weights = weights;
   p.dweights = dweights;
   p.dlogits = dlogits;
+  return launched(launch_route_back(p, static_cast<hipStream_t>(stream)));
+}
+
+int a2av_moe_route_grouped(const void* logits, int64_t logits_stride, const float* bias,
+                           int64_t tokens, int32_t E, int32_t k, int32_t groups, int32_t top_groups,
+                           int32_t group_best, int32_t scores, int32_t renormalize, float scale,
+                           int32_t dtype, int32_t* experts, float* weights, int32_t* counts,
+                           int32_t* order, int32_t* place, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+  const int64_t slots = tokens > 0 && k > 0 && tokens <= kMax31 && k <= kMax31 ? tokens * k : 0;
+  int64_t need = 0;
+  const int sizes = a2av_moe_route_workspace(tokens, E, k, &need);
+  const bool bad = sizes != A2AV_OK || logits_stride < E || logits_stride > kMax31 ||
+                   bad_groups(E, k, groups, top_groups, group_best) || bad_scores(scores, scale);
+  const int64_t z = size_of(dtype);
+  const std::initializer_list<Operand> all = {
+      matrix(logits, bad && slots > 0, bad ? 0 : tokens, logits_stride, E, z, false),
+      {bias, int64_t(E > 0 ? E : 0) * 4, false, 4, true},
+      {experts, slots * 4, true, 4},   {weights, slots * 4, true, 4},
+      {counts, int64_t(E > 0 ? E : 0) * 4, true, 4},
+      {order, slots * 4, true, 4},     {place, slots * 4, true, 4},
+      {workspace, need, true, 16}};
+  if (any_null(all)) return A2AV_ERR_NULLPTR;
+  if (!is_float(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
+  if (bad || workspace_bytes < need || bad_addresses(all)) return A2AV_ERR_INVALID_ARGS;
+  RouteParams p{};
+  p.logits = logits;
+  p.stride = logits_stride;
+  p.tokens = int32_t(tokens);
+  p.E = E;
+  p.k = k;
+  p.renorm = renormalize != 0;
+  p.dtype = dtype;
+  p.experts = experts;
+  p.weights = weights;
+  p.counts = counts;
+  p.order = order;
+  p.place = place;
+  p.hist = static_cast<int32_t*>(workspace);
+  p.groups = groups;
+  p.top_groups = top_groups;
+  p.group_best = group_best;
+  p.sigmoid = scores == A2AV_MOE_SIGMOID;
+  p.bias = bias;
+  p.scale = scale;
+  return launched(launch_route(p, static_cast<hipStream_t>(stream)));
+}
+
+int a2av_moe_route_grouped_backward(const void* logits, int64_t logits_stride, int64_t tokens,
+                                    int32_t E, int32_t k, int32_t scores, int32_t renormalize,
+                                    float scale, int32_t dtype, const int32_t* experts,
+                                    const float* weights, const float* dweights, void* dlogits,
+                                    void* stream) {
+  const int sizes = check_route_sizes(tokens, E, k);
+  const int64_t slots = sizes ? (tokens > 0) : tokens * k;
+  const bool bad = sizes != A2AV_OK || logits_stride < E || logits_stride > kMax31 ||
+                   bad_scores(scores, scale);
+  const int64_t z = size_of(dtype);
+  const std::initializer_list<Operand> all = {
+      matrix(logits, bad && slots > 0, bad ? 0 : tokens, logits_stride, E, z, false),
+      {experts, slots * 4, false, 4},
+      {weights, slots * 4, false, 4},
+      {dweights, slots * 4, false, 4},
+      {dlogits, sizes ? slots : tokens * E * z, true, z}};
+  if (any_null(all)) return A2AV_ERR_NULLPTR;
+  if (!is_float(dtype)) return A2AV_ERR_UNSUPPORTED_DTYPE;
+  if (bad || bad_addresses(all)) return A2AV_ERR_INVALID_ARGS;
+  RouteBackParams p{};
+  p.logits = logits;
+  p.stride = logits_stride;
+  p.tokens = int32_t(tokens);
+  p.E = E;
+  p.k = k;
+  p.renorm = renormalize != 0;
+  p.dtype = dtype;
+  p.experts = experts;
+  p.weights = weights;
+  p.dweights = dweights;
+  p.dlogits = dlogits;
+  p.grouped = 1;
+  p.sigmoid = scores == A2AV_MOE_SIGMOID;
+  p.scale = scale;
   return launched(launch_route_back(p, static_cast<hipStream_t>(stream)));
 }
 

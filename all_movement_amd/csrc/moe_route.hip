@@ -1,4 +1,4 @@
-// moe_route.hip -- the top-k router and its gradient.
+// moe_route.hip -- the top-k router, the router by groups, and their gradients.
 //
 // A wave takes a token: its E logits sit in the wave's registers (logit
 // PER * lane + i in register i), the k largest are taken one after the other by
@@ -254,6 +254,146 @@ __device__ inline void choose(const RouteParams& p, int t, const float (&v)[PER]
   }
 }
 
+// ------------------------------------------------------------------ the router by groups
+
+// Rising unsigned keys in the order of the numbers, NaN on top, as key_of's.
+__device__ inline uint64_t key64_of(double v) {
+  const uint64_t b = uint64_t(__double_as_longlong(v + 0.0));
+  const uint64_t key = b ^ (uint64_t(int64_t(b) >> 63) | 1ull << 63);
+  return v != v ? ~0ull : key;
+}
+__device__ inline double of_key64(uint64_t key) {
+  return __longlong_as_double(int64_t(key >> 63 ? key & ~(1ull << 63) : ~key));
+}
+
+__device__ inline uint64_t lane64(uint64_t v, int lane) {
+  return uint64_t(uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v)), lane))) |
+         uint64_t(uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v >> 32)), lane))) << 32;
+}
+__device__ inline uint64_t wave_max64(uint64_t v) {
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t u = __shfl_xor((unsigned long long)v, d);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+__device__ inline double wave_sum64(double v) {
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// One token by one wave, as the definition says it: scores in 64 bits.
+template <int PER>
+__device__ inline void choose_grouped(const RouteParams& p, int t, const float (&v)[PER],
+                                      int32_t* ids) {
+  const int lane = threadIdx.x & 63, e0 = lane * PER, size = p.E / p.groups;
+  double s[PER];
+  uint64_t key[PER], by[PER];  // of the sum with the bias; in whose order experts are taken
+  if (p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s[i] = 1.0 / (1.0 + exp(-double(v[i])));
+  } else {
+    float most = v[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) most = fmaxf(most, v[i]);
+    most = wave_fmax(most);
+    double total = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      s[i] = v[i] == -__builtin_inff() ? 0.0 : exp(double(v[i]) - double(most));
+      total += s[i];
+    }
+    total = wave_sum64(total);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s[i] /= total;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const bool here = e0 + i < p.E && v[i] != -__builtin_inff();
+    const double c = here && p.bias ? s[i] + double(p.bias[e0 + i]) : s[i];
+    key[i] = here && c != -__builtin_inf() ? key64_of(c) : 0;
+  }
+  uint64_t allowed = ~0ull;
+  if (p.groups > 1) {
+    uint64_t group_key = 0;  // of group `lane`
+    for (int g = 0; g < p.groups; ++g) {
+      uint64_t one = 0, two = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const uint64_t k = (e0 + i) / size == g ? key[i] : 0;
+        two = k > one ? one : k > two ? k : two;
+        one = k > one ? k : one;
+      }
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint64_t a = __shfl_xor((unsigned long long)one, d);
+        const uint64_t b = __shfl_xor((unsigned long long)two, d);
+        const uint64_t low = a < one ? a : one, high = b > two ? b : two;
+        one = a > one ? a : one;
+        two = low > high ? low : high;
+      }
+      if (one) {
+        double sum = one == ~0ull ? __builtin_nan("") : of_key64(one);
+        if (p.group_best == 2 && two) sum += two == ~0ull ? __builtin_nan("") : of_key64(two);
+        if (lane == g) group_key = key64_of(sum);
+      }
+    }
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const uint64_t k = lane64(group_key, g);
+      rank += k > group_key || (k == group_key && g < lane);
+    }
+    allowed = __ballot(group_key != 0 && rank < p.top_groups);
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (p.groups > 1 && !(allowed >> ((e0 + i) / size & 63) & 1)) key[i] = 0;
+    by[i] = !key[i] ? 0 : p.bias ? key[i] : key_of(v[i]);
+  }
+  int mine = -1;
+  double my_s = 0.0;
+  for (int j = 0; j < p.k; ++j) {
+    uint64_t top = 0;
+    int at = 0;
+    double top_s = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (by[i] > top) top = by[i], at = i, top_s = s[i];
+    const uint64_t most = wave_max64(top);
+    if (!most) break;
+    const int l = __ffsll((unsigned long long)__ballot(top == most)) - 1;
+    const int e = l * PER + __builtin_amdgcn_readlane(at, l);
+    const uint64_t its = lane64(uint64_t(__double_as_longlong(top_s)), l);
+    if (lane == j) {
+      mine = e;
+      my_s = __longlong_as_double(int64_t(its));
+    }
+    if (lane == l) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i == at) by[i] = 0;
+    }
+  }
+  double total = 1.0;
+  if (p.renorm) total = wave_sum64(my_s);
+  if (lane < p.k) {
+    const int64_t slot = int64_t(t) * p.k + lane;
+    p.experts[slot] = mine;
+    p.weights[slot] = mine < 0 || total == 0.0 ? 0.0f : float(double(p.scale) * my_s / total);
+    ids[lane] = mine;
+  }
+}
+
+template <int PER, bool GROUPED>
+__device__ inline void choose_token(const RouteParams& p, int t, const float (&v)[PER],
+                                    int32_t* ids) {
+  if constexpr (GROUPED)
+    choose_grouped<PER>(p, t, v, ids);
+  else
+    choose<PER>(p, t, v, ids);
+}
+
+// ------------------------------------------------------------------ the slots' order
+
 // Ranks of the slots [first, first + kThreads) of a block among the block's
 // slots of the same expert; run[e] counts those of earlier slots and is moved
 // on.  ids in LDS, -1 = empty.  All threads of the workgroup call it.
@@ -308,7 +448,7 @@ __device__ inline int first_rows(int32_t* counts, int E) {
   return all;
 }
 
-template <int PER>
+template <int PER, bool GROUPED>
 __global__ __launch_bounds__(kThreads) void route_small(const RouteParams p) {
   __shared__ int32_t ids[kRouteSmall];
   __shared__ uint16_t hist[kWaves][kMaxE];
@@ -318,7 +458,7 @@ __global__ __launch_bounds__(kThreads) void route_small(const RouteParams p) {
   for (int t = wave; t < p.tokens; t += kWaves) {
     Row<PER> row;
     row.load(p.logits, t * p.stride, p.E, p.dtype, vec);
-    choose<PER>(p, t, row.v, ids + t * p.k);
+    choose_token<PER, GROUPED>(p, t, row.v, ids + t * p.k);
   }
   for (int i = tid; i < p.E; i += kThreads) run[i] = 0;
   __syncthreads();
@@ -344,7 +484,7 @@ __global__ __launch_bounds__(kThreads) void route_small(const RouteParams p) {
 
 // Choose: p.per_block tokens; the slots' ranks in the block go to place, the
 // block's counts to hist[e][block].
-template <int PER>
+template <int PER, bool GROUPED>
 __global__ __launch_bounds__(kThreads) void route_choose(const RouteParams p, int blocks) {
   __shared__ int32_t ids[kRouteMost * 16];
   __shared__ uint16_t hist[kWaves][kMaxE];
@@ -360,7 +500,7 @@ __global__ __launch_bounds__(kThreads) void route_choose(const RouteParams p, in
     for (int t = wave; t < nt; t += kWaves) {
       row = next;
       if (t + kWaves < nt) next.load(p.logits, (t0 + t + kWaves) * p.stride, p.E, p.dtype, vec);
-      choose<PER>(p, t0 + t, row.v, ids + t * p.k);
+      choose_token<PER, GROUPED>(p, t0 + t, row.v, ids + t * p.k);
     }
     for (int i = tid; i < p.E; i += kThreads) run[i] = 0;
     __syncthreads();
@@ -491,6 +631,91 @@ __global__ __launch_bounds__(256) void route_back(const RouteBackParams p) {
   }
 }
 
+// The gradient of the router by groups.  With u = w / scale and g the slots'
+// dweights, a chosen expert's score has the gradient scale / sum of scores *
+// sum_i u_i (g_j - g_i) when renormalised (equal terms cancel exactly: one expert
+// alone gets 0), else scale * g_j; sigmoid's slope is s (1 - s), so that only the
+// chosen logits are read.  Softmax without renormalisation reaches every logit.
+template <int PER>
+__global__ __launch_bounds__(256) void route_grouped_back(const RouteBackParams p) {
+  const int lane = threadIdx.x & 63;
+  const bool all = !p.sigmoid && !p.renorm;
+  const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
+  const bool vec_out = row_pieces<PER>(p.dlogits, p.E, p.E, p.dtype);
+  const int64_t step = int64_t(gridDim.x) * 4;
+  __shared__ __attribute__((aligned(16))) float of_expert[4][64 * PER];
+  float* const mine = of_expert[threadIdx.x >> 6];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) mine[lane * PER + i] = 0.0f;
+  auto in_order = [] {  // a wave's LDS accesses are done in order: keep theirs
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  const float inverse_scale = 1.0f / p.scale;
+  for (int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); t < p.tokens; t += step) {
+    int e = -1;
+    float w = 0.0f, g = 0.0f, l = 0.0f;
+    if (lane < p.k) {
+      e = p.experts[t * p.k + lane];
+      if (e >= p.E) e = -1;
+      if (e >= 0) {
+        w = p.weights[t * p.k + lane];
+        g = p.dweights[t * p.k + lane];
+        if (p.sigmoid) l = load_value(p.logits, t * p.stride + e, p.dtype);
+      }
+    }
+    Row<PER> row;
+    if (all) row.load(p.logits, t * p.stride, p.E, p.dtype, vec);
+    float d = p.scale * g;
+    if (!all) {
+      d = g;
+      if (p.renorm) {
+        d = 0.0f;
+        for (int i = 0; i < p.k; ++i) {
+          const float wi = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), i));
+          const float gi = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), i));
+          if (wi != 0.0f) d = fmaf(wi * inverse_scale, g - gi, d);
+        }
+      }
+      if (p.sigmoid) {  // 1 - s, without a difference of near numbers
+        const float x = exp_of(-fabsf(l));
+        d *= (l > 0.0f ? x : 1.0f) / (1.0f + x);
+      }
+      d = w == 0.0f ? 0.0f : w * d;
+    }
+    in_order();
+    if (e >= 0) mine[e] = d;
+    in_order();
+    float gr[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) gr[i] = mine[lane * PER + i];
+    in_order();
+    if (e >= 0) mine[e] = 0.0f;
+    if (all) {
+      const float mean = wave_sum(e >= 0 ? w * g : 0.0f);
+      float most = row.v[0];  // of the numbers: a NaN makes the sum NaN by itself
+#pragma unroll
+      for (int i = 1; i < PER; ++i) most = fmaxf(most, row.v[i]);
+      most = wave_fmax(most);
+      float q[PER], total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        q[i] = row.v[i] == -__builtin_inff() ? 0.0f : exp_of(row.v[i] - most);
+        total += q[i];
+      }
+      total = wave_sum(total);
+      const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        q[i] *= inverse;
+        const bool none = row.v[i] == -__builtin_inff() || q[i] == 0.0f;
+        gr[i] = none ? 0.0f : q[i] * (gr[i] - mean);
+      }
+    }
+    Row<PER>::store(p.dlogits, t * p.E, p.E, p.dtype, vec_out, gr);
+  }
+}
+
 // f(std::integral_constant) with the registers per lane that E logits need.
 template <class F>
 void with_per(int E, F f) {
@@ -503,19 +728,19 @@ void with_per(int E, F f) {
 
 }  // namespace
 
-hipError_t launch_route(RouteParams p, hipStream_t stream) {
-  (void)hipGetLastError();
-  p.per_block = route_per_block(p.tokens);
+template <bool GROUPED>
+static hipError_t launch_route_of(const RouteParams& p, hipStream_t stream) {
   if (route_is_small(p.tokens, p.E, p.k)) {
     with_per(p.E, [&](auto per) {
-      route_small<decltype(per)::value><<<dim3(1), dim3(kThreads), 0, stream>>>(p);
+      route_small<decltype(per)::value, GROUPED><<<dim3(1), dim3(kThreads), 0, stream>>>(p);
     });
     return hipGetLastError();
   }
   const int blocks = route_blocks(p.tokens);
   const int grid = blocks < 65536 ? blocks : 65536;
   with_per(p.E, [&](auto per) {
-    route_choose<decltype(per)::value><<<dim3(grid), dim3(kThreads), 0, stream>>>(p, blocks);
+    route_choose<decltype(per)::value, GROUPED>
+        <<<dim3(grid), dim3(kThreads), 0, stream>>>(p, blocks);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -526,13 +751,22 @@ hipError_t launch_route(RouteParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+hipError_t launch_route(RouteParams p, hipStream_t stream) {
+  (void)hipGetLastError();
+  p.per_block = route_per_block(p.tokens);
+  return p.groups ? launch_route_of<true>(p, stream) : launch_route_of<false>(p, stream);
+}
+
 hipError_t launch_route_back(const RouteBackParams& p, hipStream_t stream) {
   if (p.tokens == 0) return hipSuccess;
   (void)hipGetLastError();
   const int64_t want = (int64_t(p.tokens) + 3) / 4;
   const int grid = int(want < 2048 ? want : 2048);  // 8 waves per SIMD
   with_per(p.E, [&](auto per) {
-    route_back<decltype(per)::value><<<dim3(grid), dim3(256), 0, stream>>>(p);
+    if (p.grouped)
+      route_grouped_back<decltype(per)::value><<<dim3(grid), dim3(256), 0, stream>>>(p);
+    else
+      route_back<decltype(per)::value><<<dim3(grid), dim3(256), 0, stream>>>(p);
   });
   return hipGetLastError();
 }

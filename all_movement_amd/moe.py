@@ -1,7 +1,8 @@
 """The operators around the exchange for torch tensors (include/a2av_moe.h).
 
 ``route`` chooses each token's experts and makes the gather list and counts
-that the exchange and the products take; ``gmm``, ``gmm_dx`` and ``gmm_dw`` are
+that the exchange and the products take, ``route_grouped`` does so by groups of
+experts, with a bias for their balance; ``gmm``, ``gmm_dx`` and ``gmm_dw`` are
 the products grouped by expert and their gradients; ``combine`` returns the
 rows to their tokens; ``mx4_quantize``, ``mx4_dequantize`` and ``gmm_mx4`` are
 the microscaled 4-bit format and the product on it; ``fp8_quantize``,
@@ -18,8 +19,8 @@ the caller's.  ``status``, an int32 tensor of one element, receives the code of 
 check on device data that failed (it is never cleared); with ``check=True`` the
 call waits and raises instead.
 
-Gradients are calls of their own (``route_backward``, ``gmm_dx``, ``gmm_dw``,
-``combine_backward``), for a training step or an autograd function to make; no
+Gradients are calls of their own (``route_backward``, ``route_grouped_backward``,
+``gmm_dx``, ``gmm_dw``, ``gmm_fp8_dx``, ``combine_backward``), for a training step or an autograd function to make; no
 call records one, so that operands that require a gradient are refused unless
 recording is off (``torch.no_grad()``).
 """
@@ -35,12 +36,14 @@ import torch
 from . import a2av
 
 MOE_EXPORTS = ["a2av_moe_route_workspace", "a2av_moe_route", "a2av_moe_route_backward",
+               "a2av_moe_route_grouped", "a2av_moe_route_grouped_backward",
                "a2av_moe_gmm", "a2av_moe_gmm_dx", "a2av_moe_gmm_dw", "a2av_moe_combine",
                "a2av_moe_combine_backward", "a2av_moe_mx4_quantize", "a2av_moe_mx4_dequantize",
                "a2av_moe_gmm_mx4", "a2av_moe_fp8_quantize", "a2av_moe_fp8_dequantize",
                "a2av_moe_fp8_quantize_weights", "a2av_moe_fp8_dequantize_weights",
                "a2av_moe_gmm_fp8", "a2av_moe_gmm_fp8_dx"]
 
+SCORES = {"softmax": 0, "sigmoid": 1}
 _DTYPE = {torch.float32: a2av.FP32, torch.float16: a2av.FP16, torch.bfloat16: a2av.BF16}
 _lib = None
 
@@ -51,11 +54,15 @@ def lib() -> ctypes.CDLL:
     if _lib is not None:
         return _lib
     L = a2av.lib()
-    vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     sig = {
         "a2av_moe_route_workspace": [i64, i32, i32, ctypes.POINTER(i64)],
         "a2av_moe_route": [vp, i64, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, i64, vp],
         "a2av_moe_route_backward": [vp, i64, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp],
+        "a2av_moe_route_grouped": [vp, i64, vp, i64, i32, i32, i32, i32, i32, i32, i32, f32, i32,
+                                   vp, vp, vp, vp, vp, vp, i64, vp],
+        "a2av_moe_route_grouped_backward": [vp, i64, i64, i32, i32, i32, i32, f32, i32, vp, vp, vp,
+                                            vp, vp],
         "a2av_moe_gmm": [vp, i64, i64, vp, vp, vp, vp, i64, i64, i32, i64, i64, i32, vp, vp],
         "a2av_moe_gmm_dx": [vp, i64, vp, vp, vp, i64, i64, i32, i64, i64, i32, vp, vp],
         "a2av_moe_gmm_dw": [vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, i64, i64, i32, i32, vp,
@@ -191,18 +198,8 @@ def route_workspace(tokens: int, experts: int, k: int) -> int:
     return n.value
 
 
-def route(logits, k: int, *, renormalize: bool = True, out: Routing | None = None,
-          workspace=None, stream=None) -> Routing:
-    """The ``k`` largest logits of each row [tokens, experts]: a :class:`Routing`."""
-    p, stride = _matrix(logits, "logits", None, _DTYPE)
-    T, E = logits.shape
-    need = route_workspace(T, E, k)
-    if logits.requires_grad:
-        _recorded()
-    dev = _device(logits, workspace, *(out or ()))
-    if _elsewhere(dev, stream):
-        with _there(dev, stream):
-            return route(logits, k, renormalize=renormalize, out=out, workspace=workspace)
+def _routing(out, workspace, need: int, T: int, E: int, k: int, dev):
+    """The outputs, their pointers, and the workspace's pointer and bytes."""
     n = T * k
     if out is None:
         ints = torch.empty(3, T, k, dtype=torch.int32, device=dev)
@@ -225,6 +222,22 @@ def route(logits, k: int, *, renormalize: bool = True, out: Routing | None = Non
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return out, ptr, wp, wn
+
+
+def route(logits, k: int, *, renormalize: bool = True, out: Routing | None = None,
+          workspace=None, stream=None) -> Routing:
+    """The ``k`` largest logits of each row [tokens, experts]: a :class:`Routing`."""
+    p, stride = _matrix(logits, "logits", None, _DTYPE)
+    T, E = logits.shape
+    need = route_workspace(T, E, k)
+    if logits.requires_grad:
+        _recorded()
+    dev = _device(logits, workspace, *(out or ()))
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return route(logits, k, renormalize=renormalize, out=out, workspace=workspace)
+    out, ptr, wp, wn = _routing(out, workspace, need, T, E, k, dev)
     st = lib().a2av_moe_route(p, stride, T, E, k, int(renormalize), _DTYPE[logits.dtype], *ptr,
                               wp, wn, _stream(dev))
     a2av._raise(st, "a2av_moe_route")
@@ -255,6 +268,72 @@ def route_backward(logits, experts, weights, dweights, *, renormalize: bool = Tr
     st = lib().a2av_moe_route_backward(p, stride, T, E, k, int(renormalize), _DTYPE[logits.dtype],
                                        *ptr, op, _stream(dev))
     a2av._raise(st, "a2av_moe_route_backward")
+    return out
+
+
+def _scores(scores: str) -> int:
+    if scores not in SCORES:
+        raise ValueError(f"scores must be one of {tuple(SCORES)}, got {scores!r}")
+    return SCORES[scores]
+
+
+def route_grouped(logits, k: int, *, scores: str = "sigmoid", bias=None, groups: int = 1,
+                  top_groups: int | None = None, group_best: int = 2, renormalize: bool = True,
+                  scale: float = 1.0, out: Routing | None = None, workspace=None,
+                  stream=None) -> Routing:
+    """The router by groups: ``k`` experts of each token out of its ``top_groups`` (default:
+    all) best groups, by ``scores`` ("sigmoid" or "softmax") plus ``bias`` (float32
+    [experts]); their weights are the scores alone, renormalised and times ``scale``.  A
+    group counts by its ``group_best`` largest.  A :class:`Routing`, as :func:`route`'s."""
+    kind = _scores(scores)
+    p, stride = _matrix(logits, "logits", None, _DTYPE)
+    T, E = logits.shape
+    if top_groups is None:
+        top_groups = groups
+    need = route_workspace(T, E, k)
+    bp = None if bias is None else _whole(bias, "bias", (E,), torch.float32)
+    if logits.requires_grad or bias is not None and bias.requires_grad:
+        _recorded()
+    dev = _device(logits, bias, workspace, *(out or ()))
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return route_grouped(logits, k, scores=scores, bias=bias, groups=groups,
+                                 top_groups=top_groups, group_best=group_best,
+                                 renormalize=renormalize, scale=scale, out=out,
+                                 workspace=workspace)
+    out, ptr, wp, wn = _routing(out, workspace, need, T, E, k, dev)
+    st = lib().a2av_moe_route_grouped(p, stride, bp, T, E, k, groups, top_groups, group_best, kind,
+                                      int(renormalize), scale, _DTYPE[logits.dtype], *ptr, wp, wn,
+                                      _stream(dev))
+    a2av._raise(st, "a2av_moe_route_grouped")
+    return out
+
+
+def route_grouped_backward(logits, experts, weights, dweights, *, scores: str = "sigmoid",
+                           renormalize: bool = True, scale: float = 1.0, out=None, stream=None):
+    """dlogits of :func:`route_grouped`'s weights; ``logits``, ``experts``, ``weights``,
+    ``scores``, ``renormalize`` and ``scale`` are the forward call's."""
+    kind = _scores(scores)
+    p, stride = _matrix(logits, "logits", None, _DTYPE)
+    T, E = logits.shape
+    k = experts.shape[-1]
+    if (logits.requires_grad or weights.requires_grad or dweights.requires_grad or
+            out is not None and out.requires_grad):
+        _recorded()
+    dev = _device(logits, experts, weights, dweights, out)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return route_grouped_backward(logits, experts, weights, dweights, scores=scores,
+                                          renormalize=renormalize, scale=scale, out=out)
+    ptr = (_whole(experts, "experts", (T, k), torch.int32),
+           _whole(weights, "weights", (T, k), torch.float32),
+           _whole(dweights, "dweights", (T, k), torch.float32))
+    if out is None:
+        out = torch.empty(T, E, dtype=logits.dtype, device=dev)
+    op = _whole(out, "out", (T, E), logits.dtype)
+    st = lib().a2av_moe_route_grouped_backward(p, stride, T, E, k, kind, int(renormalize), scale,
+                                               _DTYPE[logits.dtype], *ptr, op, _stream(dev))
+    a2av._raise(st, "a2av_moe_route_grouped_backward")
     return out
 
 

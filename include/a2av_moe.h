@@ -87,6 +87,50 @@ int a2av_moe_route_backward(const void *logits, int64_t logits_stride, int64_t t
                             const float *weights, const float *dweights, void *dlogits,
                             void *stream);
 
+/* ------------------------------------------------------ the router by groups
+ *
+ * For every token: scores s = sigmoid(logits) or softmax(logits), and with a
+ * bias, which takes part in the choice and in nothing else, c = s + bias (without
+ * one c = s).  The experts stand in `groups` groups of E / groups neighbours.  A
+ * group's score is the sum of its group_best (1 or 2) largest c, of as many as
+ * there are; the top_groups groups of the highest scores are taken, and of
+ * their experts the k of the highest c (without a bias: of the highest logits),
+ * in falling order.  Equal ones go by their lower number.  c and the groups'
+ * scores are compared in 64 bits.  A logit of -inf is not chosen, nor is a c of
+ * -inf; a group without any other is not taken; a token with fewer than k
+ * experts to choose has empty slots.  NaN ranks above every number.
+ *   weights[t][j]  scale * s of that expert, with renormalize != 0 divided by the
+ *                  sum of s over the token's chosen ones (0 where that is 0); 0
+ *                  for an empty slot
+ *   experts, counts, order, place, workspace as in a2av_moe_route
+ * bias float [E] or NULL.  Limits: as in a2av_moe_route; groups in 1..64 and a
+ * divisor of E, top_groups in 1..groups, k <= top_groups * (E / groups), scale in
+ * 2^-100..2^100.
+ */
+enum { A2AV_MOE_SOFTMAX = 0, A2AV_MOE_SIGMOID = 1 };
+
+int a2av_moe_route_grouped(const void *logits, int64_t logits_stride, const float *bias,
+                           int64_t tokens, int32_t E, int32_t k, int32_t groups, int32_t top_groups,
+                           int32_t group_best, int32_t scores, int32_t renormalize, float scale,
+                           int32_t dtype, int32_t *experts, float *weights, int32_t *counts,
+                           int32_t *order, int32_t *place, void *workspace, int64_t workspace_bytes,
+                           void *stream);
+
+/* The gradient of the weights with respect to the logits, the choice held fixed.
+ * With u = weights / scale and g = dweights, of the chosen expert of slot j
+ *   sigmoid  dlogits = weights_j (1 - s_j) (g_j - mean)
+ *   softmax  dlogits = weights_j (g_j - mean), renormalised
+ * with mean = sum_i u_i g_i when renormalised, else 0, and 0 for every other
+ * expert; softmax without renormalisation, for every expert e,
+ *   dlogits[e] = softmax_e (scale * g_e - sum_i weights_i g_i)
+ * with g_e = 0 where e is not chosen.  The bias gets none.  Operands, empty slots
+ * and experts outside [-1, E) as in a2av_moe_route_backward; a weight of 0 gives 0. */
+int a2av_moe_route_grouped_backward(const void *logits, int64_t logits_stride, int64_t tokens,
+                                    int32_t E, int32_t k, int32_t scores, int32_t renormalize,
+                                    float scale, int32_t dtype, const int32_t *experts,
+                                    const float *weights, const float *dweights, void *dlogits,
+                                    void *stream);
+
 /* ------------------------------------------------- products grouped by expert
  *
  * `rows` rows stand in expert order: the first counts[0] belong to expert 0,
