@@ -31,38 +31,46 @@ __device__ inline float4v mma_fp8(int8v a, int8v b, float4v c, int sa, int sb) {
 // Bytes of scales of a row of `blocks` blocks.
 __host__ __device__ inline int64_t scale_bytes(int64_t blocks) { return (blocks + 3) / 4 * 4; }
 
-// One operand's 128 bytes x SPAN outputs of a stage in LDS, as chunks of 16 bytes.
-//   along:  [SPAN][8 chunks], chunk c of row r at c ^ (r & 7): the 8 lanes that
-//           read 128 bytes together, one chunk of 8 rows, meet every bank once.
-//   across: [16 groups of 8 rows][SPAN / 16 chunks][8 rows]: the transposing read
-//           takes a chunk's 8 rows, 128 bytes on end, by 16 lanes.
-// A lane of group g takes the chunks (along) or rows (across) of 16 g and 64 + 16 g;
-// any share of the block is right that both operands follow.
+// One operand's 128 bytes x SPAN outputs of a stage in LDS, in lines of 128 bytes
+// whose chunk c of 16 bytes lies at c ^ (line & 7).
+//   along:  a line per output.  A fragment's lane reads the chunks g and 4 + g of its
+//           row; 8 lanes, one chunk of 8 rows, meet every bank once.
+//   across: SPAN / 128 panels of 128 lines, a line per term of the reduction.  The
+//           transposing read takes one chunk of 8 lines, by 16 lanes, from every bank
+//           once, and gives each lane the 8 terms of its output; a lane takes those
+//           of 16 g and of 64 + 16 g on.
+// Which terms a lane takes is free, as long as both operands agree.
 template <bool ALONG, int SPAN>
 struct Block {
   static constexpr int kBytes = SPAN * 128;
-  __device__ static int row(int q) {
-    return ALONG ? q / 8 : q / (SPAN / 2) * 8 + (q & 7);
-  }
+  // Chunk number q of the tile in LDS: its output or term, and its chunk in that row.
+  __device__ static int row(int q) { return ALONG ? q / 8 : q / 8 % 128; }
   __device__ static int chunk(int q) {
-    return ALONG ? (q ^ q >> 3) & 7 : q / 8 % (SPAN / 16);
+    return ((q ^ q >> 3) & 7) + (ALONG ? 0 : q / 1024 * 8);
   }
-  // The fragment of the outputs f * 16 .. + 15.
-  __device__ static int8v read(const uint8_t* at, int f) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
+  // This lane's place in the fragments of the 16 outputs `first` on, for terms from 0.
+  __device__ static uint32_t lane_at(int lane, int first) {
+    const int g = lane >> 4, l = lane & 15;
+    if (ALONG) return uint32_t((first + l) * 128 + (g ^ (l & 7)) * 16);
+    const int panel = first >> 7, c = first >> 4 & 7, line = g * 16 + (l >> 1);
+    return uint32_t(panel * 16384 + line * 128 + (c ^ (line & 7)) * 16 + (l & 1) * 8);
+  }
+  // The fragment 16 f outputs further (across: in the same panel, and `at` of a
+  // multiple of 16 f).
+  __device__ static int8v read(uint32_t at, uint32_t buffer, int f) {
     if constexpr (ALONG) {
-      const uint8_t* r = at + (f * 16 + l) * 128;
-      const int4v lo = *reinterpret_cast<const int4v*>(r + (g ^ (l & 7)) * 16);
-      const int4v hi = *reinterpret_cast<const int4v*>(r + ((4 + g) ^ (l & 7)) * 16);
+      typedef const __attribute__((address_space(3))) int4v lds_int4;
+      const int4v lo = *(lds_int4*)(uintptr_t(at + buffer + f * 2048));
+      const int4v hi = *(lds_int4*)(uintptr_t((at ^ 64) + buffer + f * 2048));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
       typedef __attribute__((address_space(3))) int2v lds_int2;
+      const uint32_t from = (at ^ uint32_t(f * 16)) + buffer;
       int8v v;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int eight = (i >> 1) * 8 + g * 2 + (i & 1);
         const int2v w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (lds_int2*)(at + eight * (SPAN * 8) + f * 128 + l * 8));
+            (lds_int2*)(uintptr_t(from + (i >> 1) * 8192 + (i & 1) * 1024)));
         v[2 * i] = w[0];
         v[2 * i + 1] = w[1];
       }
@@ -72,7 +80,7 @@ struct Block {
 };
 
 // BM x BN of the output by 2 x 2 waves, a block per step, the next one's loads on
-// their way to the other LDS buffer.
+// their way to the other LDS buffer, with 64-bit addresses for operands of any size.
 template <int MODE, int BM, int BN>
 __global__ __launch_bounds__(256) void fp8_kernel(const GmmParams p) {
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
@@ -137,6 +145,7 @@ __global__ __launch_bounds__(256) void fp8_kernel(const GmmParams p) {
   };
 
   const uint32_t lds0 = uint32_t(uintptr_t((lds_u8*)lds));
+  const uint32_t q_lane = Q::lane_at(lane, wm * TM), c_lane = C::lane_at(lane, wn * TN);
   auto issue = [&](int b) {
     const uint32_t base = lds0 + (b & 1) * kBuf;
 #pragma unroll
@@ -161,19 +170,19 @@ __global__ __launch_bounds__(256) void fp8_kernel(const GmmParams p) {
   for (int b = 0; b < steps; ++b) {
     wait_loads_and_barrier();
     if (b + 1 < steps) issue(b + 1);
-    const uint8_t* buf = lds + (b & 1) * kBuf;
+    const uint32_t buf = lds0 + (b & 1) * kBuf;
     int sc[FN], sq[FM];
     int8v fc[FN];
 #pragma unroll
     for (int d = 0; d < FN; ++d) {
       sc[d] = w_scale(b, d);
-      fc[d] = C::read(buf + Q::kBytes, wn * FN + d);
+      fc[d] = C::read(c_lane, buf + Q::kBytes, d);
     }
 #pragma unroll
     for (int a = 0; a < FM; ++a) sq[a] = qs[a] ? qs[a][b] : 127;
 #pragma unroll
     for (int a = 0; a < FM; ++a) {
-      const int8v fq = Q::read(buf, wm * FM + a);
+      const int8v fq = Q::read(q_lane, buf, a);
 #pragma unroll
       for (int d = 0; d < FN; ++d) acc[a][d] = mma_fp8(fc[d], fq, acc[a][d], sc[d], sq[a]);
     }
@@ -183,12 +192,348 @@ __global__ __launch_bounds__(256) void fp8_kernel(const GmmParams p) {
   store_tile<MODE, TM, TN, FM, FN>(p, t, acc, wm, wn);
 }
 
+// ------------------------------------------------------------------ the pipelined tile kernel
+
+// v, of which the compiler keeps nothing else across the loop: 64-bit addresses made
+// of 32-bit offsets beforehand would not fit beside the sums and fragments.
+__device__ inline uint32_t here(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// acc += a b, scaled, with the sums in the accumulation registers, or with VECTOR in
+// the vector registers.
+template <bool VECTOR>
+__device__ inline void mma_acc8(float4v& acc, const int8v& a, const int8v& b, int sa, int sb) {
+  if constexpr (VECTOR)
+    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+        : "+v"(acc)
+        : "v"(a), "v"(b), "v"(sa), "v"(sb));
+  else
+    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+        : "+a"(acc)
+        : "v"(a), "v"(b), "v"(sa), "v"(sb));
+}
+
+// A byte per lane from base + offset to the word in LDS at `to` + 4 * lane.
+__device__ inline void load_byte_to_lds(const uint8_t* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2"
+               :
+               : "s"(to), "v"(offset), "s"(base)
+               : "memory");
+}
+
+template <int BM, int BN, int NB>
+struct Pipe8 {
+  static constexpr int NW = 4, kBuf = (BM + BN) * 128;
+  // Two sets of scales of four stages: 256 rows' words, and 64 words of every wave.
+  static constexpr int kRowSet = 1024, kColSet = NW * 256, kSet = kRowSet + kColSet;
+  static constexpr int kLds = NB * kBuf + 2 * kSet;
+};
+
+// BM x BN of the output by 2 x 2 waves, one per SIMD, a block of 128 terms per stage
+// through NB LDS buffers.  A wave's products of a stage are one instruction per
+// fragment pair, in four quarters: with rows L, H and columns X, Y
+//   L X, L Y, H Y, H X    and in the next stage, X and Y changed, L Y, L X, H X, H Y.
+// Every half of the fragments stands in one set of registers and is read again in the
+// quarter after its last use: Y and H of this stage in the first two, then, past the
+// stage's one barrier, L and Y of the next.  So the reads are spread evenly (all of
+// them after the last product of a fragment would come in bursts that LDS cannot
+// serve), and two sets of them would not fit beside 256 sums.  Past the barrier nobody
+// reads the stage's buffer again and the loads of stage s + NB go there; before it
+// everybody waits for his loads of stage s + 1.
+// The rows that a tile reads lie within 4 GiB of its first.
+template <int MODE, int BM, int BN, int NB>
+__device__ inline void fp8_tile(const GmmParams& p, const Tile& t, uint8_t* lds) {
+  using Shape = Pipe8<BM, BN, NB>;
+  constexpr int NW = Shape::NW, TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
+  constexpr int HM = FM / 2, HN = FN / 2, kBuf = Shape::kBuf;
+  constexpr bool kFwd = MODE == kGmmFwd;
+  using Q = Block<true, BM>;
+  using C = Block<kFwd, BN>;
+  constexpr int kQ = BM / 8 / NW, kC = BN / 8 / NW, kAll = kQ + kC;  // loads per wave and stage
+
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int rm = __builtin_amdgcn_readfirstlane(t.rm);
+  const int cn = __builtin_amdgcn_readfirstlane(t.cn);
+  const int w_blocks = (p.N + 127) / 128;
+  const int stages = kFwd ? p.blocks : w_blocks;
+  const int64_t e_rows = int64_t(t.span.e) * p.N;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(g_zeros);
+  bool bad_row = false;
+
+  // ---- Where each chunk of this lane begins: base + offset, moved on by a uniform
+  // step per stage.  Outputs past the tile's edge read a row or chunk inside it: they
+  // are not stored.
+  constexpr uint32_t kBad = 0xffffffffu;
+  uint32_t qo[kQ], co[kC];
+  const uint8_t* qbase = p.rows + (kFwd && p.index ? 0 : t.span.row0 * p.row_stride);
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int q = (wave * kQ + i) * 64 + lane;
+    int r = Q::row(q);
+    r = r < rm ? r : rm - 1;
+    uint32_t row = uint32_t(r);
+    if (kFwd && p.index) {
+      const int64_t x = p.index[t.span.row0 + r];
+      const bool ok = x >= 0 && x < p.x_rows;
+      bad_row = bad_row || !ok;
+      row = ok ? uint32_t(x) : kBad;
+    }
+    qo[i] = row == kBad ? kBad : row * uint32_t(p.row_stride) + Q::chunk(q) * 16;
+  }
+  const uint8_t* cbase = p.other + (kFwd ? (e_rows + t.c0) * p.other_stride
+                                         : e_rows * p.other_stride + t.c0);
+  const int64_t cstep = kFwd ? 128 : 128 * p.other_stride;
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    const int q = (wave * kC + i) * 64 + lane, r = C::row(q), ch = C::chunk(q);
+    if (kFwd)
+      co[i] = uint32_t(r < cn ? r : cn - 1) * uint32_t(p.other_stride) + ch * 16;
+    else
+      co[i] = uint32_t(r) * uint32_t(p.other_stride) + (ch * 16 < cn ? ch * 16 : 0);
+  }
+  qbase = uniform(qbase);
+  cbase = uniform(cbase);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(uint32_t(uintptr_t((lds_u8*)lds)));
+  const uint32_t sets = lds0 + NB * kBuf;
+
+  // ---- Scales, four stages at a time: a word of a row by each lane, and the four
+  // stages' bytes of the weight's blocks that this wave's columns lie in.
+  const int64_t w_pitch = scale_bytes(p.blocks);
+  uint32_t row_off;
+  {
+    const int r = (wave * 64 + lane) % BM;
+    int64_t row = r < rm ? r : rm - 1;
+    if (kFwd && p.index) {
+      row = p.index[t.span.row0 + row];
+      if (row < 0 || row >= p.x_rows) row = -1;
+    }
+    row_off = row < 0 ? kBad : uint32_t(row) * uint32_t(scale_bytes(stages));
+  }
+  const uint8_t* row_scales =
+      uniform(p.row_scales + (kFwd && p.index ? 0 : t.span.row0 * scale_bytes(stages)));
+  int64_t cols = (t.c0 + wn * TN) / 128;  // of a wave past the tile's edge: the last block
+  const int64_t most = (kFwd ? w_blocks : p.blocks) - 1;
+  cols = cols < most ? cols : most;
+  const uint8_t* col_scales =
+      uniform(p.other_scales + (kFwd ? (int64_t(t.span.e) * w_blocks + cols) * w_pitch
+                                     : int64_t(t.span.e) * w_blocks * w_pitch + cols));
+  auto load_scales = [&](int group) {
+    const uint32_t to = sets + (group & 1) * Shape::kSet;
+    if (group * 4 >= stages) group = 0;  // past the end: any that there are
+    // A row outside x has zeros, and a scale that is a number.
+    const uint32_t at = here(row_off);
+    load_word_to_lds(at == kBad ? zeros : row_scales + group * 4 + at, to + wave * 256);
+    const int left = stages - 1 - group * 4, s = (lane & 3) < left ? lane & 3 : left;
+    const uint8_t* from = col_scales + group * 4 * (kFwd ? 1 : w_pitch);
+    load_byte_to_lds(from, uint32_t(s) * uint32_t(kFwd ? 1 : w_pitch),
+                     to + Shape::kRowSet + wave * 256);
+  };
+
+  // ---- load i of stage s, into buffer s % NB.  FAST: all of it exists.
+  auto load_one = [&](int s, int i, auto fast) {
+    const uint32_t to = lds0 + s % NB * kBuf +
+                        (i < kQ ? (wave * kQ + i) * 1024 : Q::kBytes + (wave * kC + i - kQ) * 1024);
+    if (i < kQ) {
+      const uint8_t* from = qbase + int64_t(s) * 128;
+      if constexpr (decltype(fast)::value)
+        load_to_lds(from, qo[i], to);
+      else
+        load_to_lds(s < stages && qo[i] != kBad ? from + here(qo[i]) : zeros, to);
+    } else {
+      const int j = i - kQ;
+      const uint8_t* from = cbase + s * cstep;
+      if constexpr (decltype(fast)::value) {
+        load_to_lds(from, co[j], to);
+      } else {
+        const int term = kFwd ? s * 128 : s * 128 + C::row((wave * kC + j) * 64 + lane);
+        load_to_lds(term < (kFwd ? stages * 128 : p.N) ? from + here(co[j]) : zeros, to);
+      }
+    }
+  };
+  constexpr auto kFast = std::true_type{};
+  constexpr auto kCareful = std::false_type{};
+
+  float4v acc[FM][FN];
+#pragma unroll
+  for (int a = 0; a < FM; ++a)
+#pragma unroll
+    for (int b = 0; b < FN; ++b) acc[a][b] = float4v{0, 0, 0, 0};
+  int8v fq[FM], fc[FN];
+  int sq[FM], sc, next_sc;
+  const uint32_t q_lane = Q::lane_at(lane, wm * TM), c_lane = C::lane_at(lane, wn * TN);
+  const uint32_t s_lane = (wm * TM + l16) * 4;
+  typedef const __attribute__((address_space(3))) uint8_t lds_byte;
+  typedef const __attribute__((address_space(3))) int lds_word;
+  auto read_q = [&](int f, int s, uint32_t buffer) {
+    fq[f] = Q::read(q_lane, buffer, f);
+    sq[f] = *(lds_byte*)(uintptr_t(sets + (s >> 2 & 1) * Shape::kSet + s_lane + (s & 3) + f * 64));
+  };
+  auto read_c = [&](int f, uint32_t buffer) { fc[f] = C::read(c_lane, buffer + Q::kBytes, f); };
+  auto read_sc = [&](int s) {
+    next_sc = *(lds_word*)(uintptr_t(sets + (s >> 2 & 1) * Shape::kSet + Shape::kRowSet +
+                                     wave * 256 + (s & 3) * 4));
+  };
+
+  load_scales(0);
+#pragma unroll
+  for (int s = 0; s < NB; ++s)
+#pragma unroll
+    for (int i = 0; i < kAll; ++i) load_one(s, i, kCareful);
+  // A wave that names a row outside x takes the careful loads throughout.
+  const bool careful = __ballot(bad_row) != 0;
+  wait_loads<(NB - 1) * kAll>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read_sc(0);
+#pragma unroll
+  for (int f = 0; f < HN; ++f) read_c(f, lds0);
+#pragma unroll
+  for (int f = 0; f < HM; ++f) read_q(f, 0, lds0);
+  sc = next_sc;
+
+  // Sums from kVector on stay in vector registers: with all 256 accumulation
+  // registers of a lane taken the compiler moves sums about between products.
+  constexpr int kVector = FM * FN < 64 ? FM * FN : 58;
+  constexpr int kQuarter = HM * HN;
+  auto stage = [&](int s, auto parity, auto fast) {
+    constexpr int X = decltype(parity)::value, Y = 1 - X;
+    const uint32_t now = lds0 + s % NB * kBuf, next = lds0 + (s + 1) % NB * kBuf;
+    // Whatever the compiler does to the registers is done before the first product,
+    // with the distance that products need.
+#pragma unroll
+    for (int f = 0; f < HM; ++f) asm volatile("" : "+v"(fq[f]), "+v"(sq[f]));
+#pragma unroll
+    for (int f = 0; f < HN; ++f) asm volatile("" : "+v"(fc[X * HN + f]));
+    asm volatile("s_nop 1" : "+v"(sc));
+    __builtin_amdgcn_sched_barrier(0);
+    each(std::make_integer_sequence<int, 4>{}, [&](auto quarter) {
+      constexpr int qt = decltype(quarter)::value;
+      constexpr int a0 = qt < 2 ? 0 : HM, b0 = (qt == 1 || qt == 2 ? Y : X) * HN;
+      if constexpr (qt == 2) {
+        // The loads of stage s + 1 and all before them have arrived.
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NB - 2) * kAll) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if ((s & 3) == 0) load_scales((s >> 2) + 1);
+        read_sc(s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int n = 0; n < kQuarter; ++n) {
+        const int a = a0 + n / HN, b = b0 + n % HN;
+        if (a * FN + b >= kVector)
+          mma_acc8<true>(acc[a][b], fc[b], fq[a], sc, sq[a]);
+        else
+          mma_acc8<false>(acc[a][b], fc[b], fq[a], sc, sq[a]);
+        __builtin_amdgcn_sched_barrier(0);
+        // The compiler would put each read right before its use: it keeps this order.
+        constexpr int kReads = qt == 0 || qt == 3 ? HN : HM;
+#pragma unroll
+        for (int r = 0; r < kReads; ++r)
+          if (n == r * (kQuarter * 3 / 4) / kReads) {
+            if constexpr (qt == 0) read_c(Y * HN + r, now);
+            if constexpr (qt == 1) read_q(HM + r, s, now);
+            if constexpr (qt == 2) read_q(r, s + 1, next);
+            if constexpr (qt == 3) read_c(Y * HN + r, next);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        if constexpr (qt >= 2) {
+#pragma unroll
+          for (int i = 0; i < kAll; ++i)
+            if ((qt - 2) * kQuarter + n == i * 2 * kQuarter / kAll) {
+              load_one(s + NB, i, fast);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+      }
+    });
+    end_of_products();
+    sc = next_sc;
+  };
+  constexpr auto kEven = std::integral_constant<int, 0>{};
+  constexpr auto kOdd = std::integral_constant<int, 1>{};
+  int s = 0;
+  const int whole = kFwd ? stages : p.N / 128;  // stages that exist to their end
+  if (!careful)
+    for (; s + 1 + NB < whole; s += 2) {
+      stage(s, kEven, kFast);
+      stage(s + 1, kOdd, kFast);
+    }
+  for (; s < stages; s += 2) {
+    stage(s, kEven, kCareful);
+    if (s + 1 < stages) stage(s + 1, kOdd, kCareful);
+  }
+  // The loads still in flight write to this workgroup's LDS; the last products have
+  // to end before their sums are read.
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int a = 0; a < FM; ++a)
+#pragma unroll
+    for (int b = 0; b < FN; ++b) {
+      if (a * FN + b >= kVector)
+        asm volatile("" : "+v"(acc[a][b]));
+      else
+        asm volatile("" : "+a"(acc[a][b]));
+    }
+  if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
+  __syncthreads();  // everybody's reads and loads are done
+  constexpr int kPart = NB * kBuf / NW / 1024 * 1024;
+  if (p.out_type == A2AV_FP32)
+    store_rows<MODE, TM, TN, FM, FN, 4, kPart>(p, t, acc, wm, wn, lds + wave * kPart);
+  else
+    store_rows<MODE, TM, TN, FM, FN, 2, kPart>(p, t, acc, wm, wn, lds + wave * kPart);
+}
+
+// 256 x 256 tiles, one workgroup per CU.
+template <int MODE>
+__global__ __launch_bounds__(256, 1) void fp8_large(const GmmParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Pipe8<256, 256, 2>::kLds];
+  static_assert(Pipe8<128, 128, 4>::kLds <= sizeof(lds), "quarters fit");
+  Tile t;
+  int part;
+  if (!find_work<MODE, 256, 256, true>(p, &t, &part)) return;
+  if (part < 0)
+    fp8_tile<MODE, 256, 256, 2>(p, t, lds);
+  else
+    fp8_tile<MODE, 128, 128, 4>(p, t, lds);
+}
+
+// 128 x 128 tiles, two workgroups per CU (NB = 2) or one.
+template <int MODE, int NB>
+__global__ __launch_bounds__(256, NB == 2 ? 2 : 1) void fp8_small(const GmmParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Pipe8<128, 128, NB>::kLds];
+  Tile t;
+  int part;
+  if (!find_work<MODE, 128, 128, false>(p, &t, &part)) return;
+  fp8_tile<MODE, 128, 128, NB>(p, t, lds);
+}
+
+template <int MODE>
+hipError_t launch_mode(const GmmParams& p, hipStream_t stream) {
+  // The pipelined kernels go by 32-bit offsets from a tile's first row (x that the
+  // forward product gathers: from its first).
+  const int64_t far = (int64_t(1) << 32) - 256;
+  const bool near = p.row_stride <= far / 256 && p.other_stride <= far / 256 &&
+                    (MODE != kGmmFwd || !p.index || p.row_stride <= far / (p.x_rows + 1));
+  if (near) {
+    if (p.nrows / p.E >= 160)
+      return launch_tiles<MODE, 256, 256>(fp8_large<MODE>, 256, p, stream);
+    const int64_t cols = MODE == kGmmFwd ? p.N : p.K;
+    if (expected_row_tiles(p, 128) * ((cols + 127) / 128) > 256)
+      return launch_tiles<MODE, 128, 128>(fp8_small<MODE, 2>, 256, p, stream);
+    return launch_tiles<MODE, 128, 128>(fp8_small<MODE, 4>, 256, p, stream);
+  }
+  return launch_tiles<MODE, 128, 128>(fp8_kernel<MODE, 128, 128>, 256, p, stream);
+}
+
 }  // namespace
 
 hipError_t launch_gmm_fp8(const GmmParams& p, GmmMode mode, hipStream_t stream) {
-  if (mode == kGmmFwd)
-    return launch_tiles<kGmmFwd, 128, 128>(fp8_kernel<kGmmFwd, 128, 128>, 256, p, stream);
-  return launch_tiles<kGmmDx, 128, 128>(fp8_kernel<kGmmDx, 128, 128>, 256, p, stream);
+  return mode == kGmmFwd ? launch_mode<kGmmFwd>(p, stream) : launch_mode<kGmmDx>(p, stream);
 }
 
 }  // namespace a2av
