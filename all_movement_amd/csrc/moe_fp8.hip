@@ -28,6 +28,14 @@ __device__ inline float4v mma_fp8(int8v a, int8v b, float4v c, int sa, int sb) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
 }
 
+// As end_of_products, for an instruction of eight passes: its sums may be looked at
+// twelve wait states later, and branches are no part of the compiler's count.
+__device__ inline void end_of_blocks() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Bytes of scales of a row of `blocks` blocks.
 __host__ __device__ inline int64_t scale_bytes(int64_t blocks) { return (blocks + 3) / 4 * 4; }
 
@@ -186,7 +194,7 @@ __global__ __launch_bounds__(256) void fp8_kernel(const GmmParams p) {
 #pragma unroll
       for (int d = 0; d < FN; ++d) acc[a][d] = mma_fp8(fc[d], fq, acc[a][d], sc[d], sq[a]);
     }
-    end_of_products();
+    end_of_blocks();
   }
   if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
   store_tile<MODE, TM, TN, FM, FN>(p, t, acc, wm, wn);
@@ -420,6 +428,9 @@ __device__ inline void fp8_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
         asm volatile("" ::: "memory");
         if ((s & 3) == 0) load_scales((s >> 2) + 1);
         read_sc(s + 1);
+#pragma unroll
+        for (int f = HM; f < FM; ++f) asm volatile("" : "+v"(fq[f]), "+v"(sq[f]));
+        asm volatile("s_nop 1");
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -451,7 +462,6 @@ __device__ inline void fp8_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
         }
       }
     });
-    end_of_products();
     sc = next_sc;
   };
   constexpr auto kEven = std::integral_constant<int, 0>{};
@@ -512,22 +522,178 @@ __global__ __launch_bounds__(256, NB == 2 ? 2 : 1) void fp8_small(const GmmParam
   fp8_tile<MODE, 128, 128, NB>(p, t, lds);
 }
 
+// ------------------------------------------------------------------ few rows per expert
+
+// MT x 16 rows and FN x 16 columns by NW waves that share out the reduction.  With few
+// rows a weight's bytes are the time: every wave streams its part of W straight into
+// registers, U blocks of its rows at a time, and the waves' sums meet in LDS, in the
+// order of the waves.  A group of four blocks has its scales in one word of a row and
+// one of the weight's.  32 rows of 8 experts, 2048 x 7168: 26 us, 4.6 TB/s of W.
+// Non-temporal loads, which give up the second half of a line, took 30.
+template <int MT, int FN, int NW>
+__global__ __launch_bounds__(NW * 64, 4) void fp8_few(const GmmParams p) {
+  constexpr int BM = MT * 16, BN = FN * 16, U = 4;
+  static_assert(BN <= 128 && 128 % BN == 0, "one scale for the tile's columns");
+  __shared__ float part[NW][MT * FN][64 * 4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, l16 = lane & 15;
+  Tile t;
+  int cut;
+  if (!find_work<kGmmFwd, BM, BN, false>(p, &t, &cut)) return;
+  const int64_t w0 = int64_t(t.span.e) * p.N + t.c0;
+
+  // A row outside x reads row 0 and is made zeros before the products, as in the tile
+  // kernels, so that W's NaN show in it with every kernel.
+  const uint8_t* x[MT];
+  const uint8_t* xs[MT];
+  int mask[MT];
+  bool bad_row = false;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int r = i * 16 + l16;
+    int64_t row = t.span.row0 + (r < t.rm ? r : t.rm - 1);
+    mask[i] = -1;
+    if (p.index) {
+      row = p.index[row];
+      if (row < 0 || row >= p.x_rows) {
+        row = 0;
+        mask[i] = 0;
+        bad_row = true;
+      }
+    }
+    x[i] = p.rows + row * p.row_stride + g * 16;
+    xs[i] = p.row_scales + row * scale_bytes(p.blocks);
+  }
+  const uint8_t* w[FN];
+#pragma unroll
+  for (int f = 0; f < FN; ++f) {
+    const int c = f * 16 + l16;
+    w[f] = p.other + (w0 + (c < t.cn ? c : t.cn - 1)) * p.other_stride + g * 16;
+  }
+  const uint8_t* ws = uniform(p.other_scales + (int64_t(t.span.e) * ((p.N + 127) / 128) + t.c0 / 128) *
+                                                   scale_bytes(p.blocks));
+  float4v acc[MT][FN];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int f = 0; f < FN; ++f) acc[i][f] = float4v{0, 0, 0, 0};
+
+  auto load = [&](const uint8_t* from) {
+    const int4v lo = *reinterpret_cast<const int4v*>(from);
+    const int4v hi = *reinterpret_cast<const int4v*>(from + 64);
+    return int8v(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  // Blocks first .. first + n of a group of four; `first` is a multiple of four.
+  auto run = [&](int first, auto n) {
+    constexpr int kN = decltype(n)::value;
+    int8v wv[kN][FN], xv[kN][MT];
+    int xg[MT];
+    const int wg = *reinterpret_cast<const int*>(ws + first);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) xg[i] = *reinterpret_cast<const int*>(xs[i] + first);
+#pragma unroll
+    for (int u = 0; u < kN; ++u) {
+#pragma unroll
+      for (int f = 0; f < FN; ++f) wv[u][f] = load(w[f] + int64_t(first + u) * 128);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) xv[u][i] = load(x[i] + int64_t(first + u) * 128);
+    }
+    each(std::make_integer_sequence<int, kN>{}, [&](auto block) {
+      constexpr int u = decltype(block)::value;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int8v row = xv[u][i] & mask[i];
+#pragma unroll
+        for (int f = 0; f < FN; ++f)  // row 0's scale may be NaN
+          acc[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              wv[u][f], row, acc[i][f], 0, 0, u, wg, u, xg[i] & mask[i]);
+      }
+    });
+    end_of_blocks();
+  };
+  // Waves take groups of U blocks in turn.
+  const int groups = p.blocks / U;
+  for (int s = wave; s < groups; s += NW) run(s * U, std::integral_constant<int, U>{});
+  if (groups % NW == wave) {
+    const int left = p.blocks - groups * U;
+    if (left == 1) run(groups * U, std::integral_constant<int, 1>{});
+    if (left == 2) run(groups * U, std::integral_constant<int, 2>{});
+    if (left == 3) run(groups * U, std::integral_constant<int, 3>{});
+  }
+  if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
+
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+      *reinterpret_cast<float4v*>(&part[wave][i * FN + f][lane * 4]) = acc[i][f];
+  __syncthreads();
+  // Element (r, c): column c % 16 = 4g + j of fragment (r / 16, c / 16), lane 16 g + r % 16.
+  for (int q = tid; q < BM * BN; q += NW * 64) {
+    const int r = q / BN, c = q % BN;
+    if (r >= t.rm || c >= t.cn) continue;
+    const int at = ((c & 15) >> 2) * 64 + (r & 15) * 4 + (c & 3);
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) v += part[i][(r >> 4) * FN + (c >> 4)][at];
+    const int64_t o = (t.out_row0 + r) * p.out_stride + t.c0 + c;
+    if (p.out_type == A2AV_FP32)
+      reinterpret_cast<float*>(p.out)[o] = v;
+    else
+      reinterpret_cast<uint16_t*>(p.out)[o] = round16(v, p.out_type);
+  }
+}
+
+template <int MT, int FN>
+hipError_t launch_few(const GmmParams& p, hipStream_t stream) {
+  // Waves that have a group of four blocks each, as far as there are any.
+  if (p.blocks > 16)
+    return launch_tiles<kGmmFwd, MT * 16, FN * 16>(fp8_few<MT, FN, 8>, 512, p, stream);
+  return launch_tiles<kGmmFwd, MT * 16, FN * 16>(fp8_few<MT, FN, 4>, 256, p, stream);
+}
+
 template <int MODE>
 hipError_t launch_mode(const GmmParams& p, hipStream_t stream) {
+  // Rules by measurement over 300 sizes drawn at random (1 to 64 experts of 1 to 300
+  // rows, some with hot ones, N to 4096, K to 7168), where the kernel chosen takes 1.04
+  // times the fastest one's time in the geometric mean, and 22 sizes are more than a
+  // tenth off.
+  if constexpr (MODE == kGmmFwd) {
+    // The streaming kernel has more and smaller workgroups than the tiles, each with the
+    // whole latency of its part in it: it pays up to three on every CU.  The tile
+    // kernels alone take 1.60 times the fastest's time, without the 16 x 16 form 1.12.
+    // us of it and of the tiles: 32 rows of 8 experts, 2048 x 7168, 26 and 34; 256 rows
+    // 33 and 35; 512 rows 57 and 38; one row, one expert 10 and 30; 256 rows of 64
+    // experts, 2048 x 2048, 49 and 55, 768 rows 56 and 55.
+    const auto wgs = [&](int BM, int BN) {
+      return expected_row_tiles(p, BM) * ((int64_t(p.N) + BN - 1) / BN);
+    };
+    if (p.x_rows > 0) {  // it reads row 0 for rows outside x
+      if (wgs(16, 16) <= 768) return launch_few<1, 1>(p, stream);
+      if (p.nrows <= int64_t(p.E) * 8) return launch_few<1, 2>(p, stream);
+      if (wgs(32, 32) <= 768) return launch_few<2, 2>(p, stream);
+    }
+  }
   // The pipelined kernels go by 32-bit offsets from a tile's first row (x that the
   // forward product gathers: from its first).
   const int64_t far = (int64_t(1) << 32) - 256;
   const bool near = p.row_stride <= far / 256 && p.other_stride <= far / 256 &&
                     (MODE != kGmmFwd || !p.index || p.row_stride <= far / (p.x_rows + 1));
-  if (near) {
-    if (p.nrows / p.E >= 160)
-      return launch_tiles<MODE, 256, 256>(fp8_large<MODE>, 256, p, stream);
-    const int64_t cols = MODE == kGmmFwd ? p.N : p.K;
-    if (expected_row_tiles(p, 128) * ((cols + 127) / 128) > 256)
-      return launch_tiles<MODE, 128, 128>(fp8_small<MODE, 2>, 256, p, stream);
-    return launch_tiles<MODE, 128, 128>(fp8_small<MODE, 4>, 256, p, stream);
-  }
-  return launch_tiles<MODE, 128, 128>(fp8_kernel<MODE, 128, 128>, 256, p, stream);
+  if (!near) return launch_tiles<MODE, 128, 128>(fp8_kernel<MODE, 128, 128>, 256, p, stream);
+  // us of the large tiles and the small ones: 2048 rows of 8 experts, 2048 x 7168, 46 and
+  // 45, dx 41 and 52; 1280 rows 38 and 37, 40 and 44; 10240 rows of 64, 2048 x 2048, 88
+  // and 94, 88 and 90; 6144 rows 82 and 65, 83 and 65.
+  if (p.nrows / p.E >= 256)
+    return launch_tiles<MODE, 256, 256>(fp8_large<MODE>, 256, p, stream);
+  // More tiles than CUs, or few stages: two workgroups on each hide each other's ends.
+  // Else one, with four stages of loads in flight.  us of two stages and four: 32 rows of
+  // 8 experts, 2048 x 7168 (128 tiles), 55 and 34, dx (448) 28 and 31; 768 rows of 64,
+  // 2048 x 2048 (1024), 55 and 63; 1540 of 7, 1001 x 523 (5 stages), 12.6 and 13.6.
+  const int64_t cols = MODE == kGmmFwd ? p.N : p.K, red = MODE == kGmmFwd ? p.K : p.N;
+  if (red <= 8 * 128 || expected_row_tiles(p, 128) * ((cols + 127) / 128) > 256)
+    return launch_tiles<MODE, 128, 128>(fp8_small<MODE, 2>, 256, p, stream);
+  return launch_tiles<MODE, 128, 128>(fp8_small<MODE, 4>, 256, p, stream);
 }
 
 }  // namespace
