@@ -188,12 +188,15 @@ __device__ inline bool row_pieces(const void* p, int64_t stride, int E, int dtyp
          reinterpret_cast<uintptr_t>(p) % uintptr_t(piece) == 0;
 }
 
-// One token by one wave: writes experts and weights, and the experts to LDS.
+// The k largest of a wave's values, in falling order, equal ones by their number:
+// lane j gets the j-th, its number in `mine` and its key, -1 where there is none left
+// but -inf.  Returns the key of the largest that is left.
 template <int PER>
-__device__ inline void choose(const RouteParams& p, int t, const float (&v)[PER], int32_t* ids) {
+__device__ inline uint32_t take_largest(const float (&v)[PER], int k, int& mine,
+                                        uint32_t& mine_key) {
   const int lane = threadIdx.x & 63;
   // Each lane's keys in falling order, equal ones in their own (neighbours
-  // change places only when out of order), and which logits they were, 4 bits
+  // change places only when out of order), and which values they were, 4 bits
   // each: the choice below looks at first keys alone.
   uint32_t key[PER];
   int id[PER];
@@ -218,9 +221,9 @@ __device__ inline void choose(const RouteParams& p, int t, const float (&v)[PER]
   if (PER <= 8) ids_left = uint32_t(ids_left);
 
   // Lane j keeps slot j: the largest first key, of the first lane that has it.
-  int mine = -1;
-  uint32_t mine_key = 0;
-  for (int j = 0; j < p.k; ++j) {
+  mine = -1;
+  mine_key = 0;
+  for (int j = 0; j < k; ++j) {
     const uint32_t m = wave_max(key[0]);
     if (m <= kNoKey) break;
     const int l = __ffsll((unsigned long long)__ballot(key[0] == m)) - 1;
@@ -237,6 +240,16 @@ __device__ inline void choose(const RouteParams& p, int t, const float (&v)[PER]
       else ids_left >>= 4;
     }
   }
+  return key[0];
+}
+
+// One token by one wave: writes experts and weights, and the experts to LDS.
+template <int PER>
+__device__ inline void choose(const RouteParams& p, int t, const float (&v)[PER], int32_t* ids) {
+  const int lane = threadIdx.x & 63;
+  int mine;
+  uint32_t mine_key;
+  take_largest<PER>(v, p.k, mine, mine_key);
   const float most = of_key(uint32_t(__builtin_amdgcn_readlane(int(mine_key), 0)));
   const float picked = mine >= 0 ? exp_of(of_key(mine_key) - most) : 0.0f;
   float total = picked;
@@ -271,126 +284,336 @@ __device__ inline uint64_t lane64(uint64_t v, int lane) {
          uint64_t(uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v >> 32)), lane))) << 32;
 }
 __device__ inline uint64_t wave_max64(uint64_t v) {
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t u = __shfl_xor((unsigned long long)v, d);
-    v = u > v ? u : v;
-  }
-  return v;
+  const uint32_t hi = wave_max(uint32_t(v >> 32));
+  const uint32_t lo = wave_max(uint32_t(v >> 32) == hi ? uint32_t(v) : 0u);
+  return uint64_t(hi) << 32 | lo;
 }
 __device__ inline double wave_sum64(double v) {
   for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
   return v;
 }
 
-// One token by one wave, as the definition says it: scores in 64 bits.
-template <int PER>
-__device__ inline void choose_grouped(const RouteParams& p, int t, const float (&v)[PER],
-                                      int32_t* ids) {
-  const int lane = threadIdx.x & 63, e0 = lane * PER, size = p.E / p.groups;
-  double s[PER];
-  uint64_t key[PER], by[PER];  // of the sum with the bias; in whose order experts are taken
-  if (p.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) s[i] = 1.0 / (1.0 + exp(-double(v[i])));
-  } else {
-    float most = v[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i) most = fmaxf(most, v[i]);
-    most = wave_fmax(most);
-    double total = 0.0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      s[i] = v[i] == -__builtin_inff() ? 0.0 : exp(double(v[i]) - double(most));
-      total += s[i];
+// One token by one wave, as the definition says it: scores in 64 bits.  They stand in
+// LDS, so that few registers are taken from the path that nearly every token goes.
+__device__ inline void choose_grouped(const RouteParams& p, int t, int32_t* ids, float* scratch) {
+  const int lane = threadIdx.x & 63, size = p.E / p.groups;
+  uint64_t* const keys = reinterpret_cast<uint64_t*>(scratch);  // 0: not to be chosen
+  auto in_order = [] {  // a wave's LDS accesses are done in order: keep theirs
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  auto logit = [&](int e) { return load_value(p.logits, int64_t(t) * p.stride + e, p.dtype); };
+  double most = 0.0, sum_of_exp = 1.0;
+  if (!p.sigmoid) {
+    float top = -__builtin_inff();
+    for (int e = lane; e < p.E; e += 64) top = fmaxf(top, logit(e));
+    most = double(wave_fmax(top));
+    sum_of_exp = 0.0;
+    for (int e = lane; e < p.E; e += 64) {
+      const float l = logit(e);
+      sum_of_exp += l == -__builtin_inff() ? 0.0 : exp(double(l) - most);
     }
-    total = wave_sum64(total);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) s[i] /= total;
+    sum_of_exp = wave_sum64(sum_of_exp);
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const bool here = e0 + i < p.E && v[i] != -__builtin_inff();
-    const double c = here && p.bias ? s[i] + double(p.bias[e0 + i]) : s[i];
-    key[i] = here && c != -__builtin_inf() ? key64_of(c) : 0;
+  auto score = [&](float l) {
+    const double x = exp(p.sigmoid ? -double(l) : double(l) - most);
+    return p.sigmoid ? 1.0 / (1.0 + x) : x / sum_of_exp;
+  };
+  in_order();
+  for (int e = lane; e < p.E; e += 64) {
+    const float l = logit(e);
+    const double c = p.bias ? score(l) + double(p.bias[e]) : score(l);
+    keys[e] = l == -__builtin_inff() || c == -__builtin_inf() ? 0 : key64_of(c);
   }
+  in_order();
   uint64_t allowed = ~0ull;
   if (p.groups > 1) {
-    uint64_t group_key = 0;  // of group `lane`
-    for (int g = 0; g < p.groups; ++g) {
-      uint64_t one = 0, two = 0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const uint64_t k = (e0 + i) / size == g ? key[i] : 0;
+    int span = 64;  // lanes of a group
+    while (span * p.groups > 64) span >>= 1;
+    const int g = lane / span;
+    uint64_t one = 0, two = 0;
+    if (g < p.groups)
+      for (int i = lane & (span - 1); i < size; i += span) {
+        const uint64_t k = keys[g * size + i];
         two = k > one ? one : k > two ? k : two;
         one = k > one ? k : one;
       }
-      for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t a = __shfl_xor((unsigned long long)one, d);
-        const uint64_t b = __shfl_xor((unsigned long long)two, d);
-        const uint64_t low = a < one ? a : one, high = b > two ? b : two;
-        one = a > one ? a : one;
-        two = low > high ? low : high;
-      }
-      if (one) {
-        double sum = one == ~0ull ? __builtin_nan("") : of_key64(one);
-        if (p.group_best == 2 && two) sum += two == ~0ull ? __builtin_nan("") : of_key64(two);
-        if (lane == g) group_key = key64_of(sum);
-      }
+    for (int d = 1; d < span; d <<= 1) {
+      const uint64_t a = __shfl_xor((unsigned long long)one, d);
+      const uint64_t b = __shfl_xor((unsigned long long)two, d);
+      const uint64_t low = a < one ? a : one, high = b > two ? b : two;
+      one = a > one ? a : one;
+      two = low > high ? low : high;
+    }
+    uint64_t group_key = 0;
+    if (one) {
+      double sum = one == ~0ull ? __builtin_nan("") : of_key64(one);
+      if (p.group_best == 2 && two) sum += two == ~0ull ? __builtin_nan("") : of_key64(two);
+      group_key = key64_of(sum);
     }
     int rank = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      const uint64_t k = lane64(group_key, g);
-      rank += k > group_key || (k == group_key && g < lane);
+    for (int i = 0; i < p.groups; ++i) {
+      const uint64_t k = lane64(group_key, i * span);
+      rank += k > group_key || (k == group_key && i < g);
     }
-    allowed = __ballot(group_key != 0 && rank < p.top_groups);
+    const uint64_t lanes = __ballot(group_key != 0 && rank < p.top_groups);
+    allowed = 0;
+    for (int i = 0; i < p.groups; ++i) allowed |= (lanes >> (i * span) & 1) << i;
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (p.groups > 1 && !(allowed >> ((e0 + i) / size & 63) & 1)) key[i] = 0;
-    by[i] = !key[i] ? 0 : p.bias ? key[i] : key_of(v[i]);
+  // In whose order experts are taken, 0 for those of other groups.
+  for (int e = lane; e < p.E; e += 64) {
+    const bool ok = keys[e] && allowed >> (p.groups > 1 ? e / size : 0) & 1;
+    if (!ok) keys[e] = 0;
+    else if (!p.bias) keys[e] = key_of(logit(e));
   }
+  in_order();
   int mine = -1;
-  double my_s = 0.0;
   for (int j = 0; j < p.k; ++j) {
     uint64_t top = 0;
     int at = 0;
-    double top_s = 0.0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (by[i] > top) top = by[i], at = i, top_s = s[i];
-    const uint64_t most = wave_max64(top);
-    if (!most) break;
-    const int l = __ffsll((unsigned long long)__ballot(top == most)) - 1;
-    const int e = l * PER + __builtin_amdgcn_readlane(at, l);
-    const uint64_t its = lane64(uint64_t(__double_as_longlong(top_s)), l);
-    if (lane == j) {
-      mine = e;
-      my_s = __longlong_as_double(int64_t(its));
+    for (int e = lane; e < p.E; e += 64) {
+      const uint64_t k = keys[e];
+      if (k > top) top = k, at = e;
     }
-    if (lane == l) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i == at) by[i] = 0;
-    }
+    const uint64_t first = wave_max64(top);
+    if (!first) break;
+    const int e = int(~wave_max(top == first ? ~uint32_t(at) : 0u));  // the lowest of them
+    if (lane == j) mine = e;
+    if (top == first && at == e) keys[e] = 0;
   }
+  const double s = mine >= 0 ? score(logit(mine)) : 0.0;
   double total = 1.0;
-  if (p.renorm) total = wave_sum64(my_s);
+  if (p.renorm) total = wave_sum64(s);
   if (lane < p.k) {
     const int64_t slot = int64_t(t) * p.k + lane;
     p.experts[slot] = mine;
-    p.weights[slot] = mine < 0 || total == 0.0 ? 0.0f : float(double(p.scale) * my_s / total);
+    p.weights[slot] = mine < 0 || total == 0.0 ? 0.0f : float(double(p.scale) * s / total);
     ids[lane] = mine;
   }
 }
 
-template <int PER, bool GROUPED>
-__device__ inline void choose_token(const RouteParams& p, int t, const float (&v)[PER],
-                                    int32_t* ids) {
-  if constexpr (GROUPED)
-    choose_grouped<PER>(p, t, v, ids);
+// A lane's value from the lane that its own number with the bits of D (1 to 8) changed
+// names, where the lanes of each smaller block hold one value already: moves inside
+// rows of 16, mirrored halves and rows doing for 4 and 8.
+template <int D>
+__device__ inline float other_lanes(float v) {
+  constexpr int kCtrl = D == 1 ? 0xb1 : D == 2 ? 0x4e : D == 4 ? 0x141 : 0x140;
+  if constexpr (D <= 8)
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
   else
-    choose<PER>(p, t, v, ids);
+    return __shfl_xor(v, D);
 }
+
+// The largest two of the values of blocks of `span` lanes (a power of two).
+template <int D>
+__device__ inline void join_best(float& one, float& two, int span) {
+  if (D < span) {
+    const float a = other_lanes<D>(one), b = other_lanes<D>(two);
+    two = fmaxf(fminf(one, a), fmaxf(two, b));
+    one = fmaxf(one, a);
+    if constexpr (D < 32) join_best<D * 2>(one, two, span);
+  }
+}
+
+// What a wave keeps over its tokens: the bias of its experts, and how groups lie in it.
+template <int PER>
+struct Groups {
+  float bias[PER];
+  uint64_t number = 0;   // the PER experts' groups after the first's, 4 bits each
+  int first;             // group of the lane's first expert
+  int span;              // lanes of a group, when they hold nothing else; else 0
+  int size;
+
+  __device__ void init(const RouteParams& p) {
+    const int lane = threadIdx.x & 63, e0 = lane * PER;
+    size = p.E / p.groups;
+    first = e0 / size;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      bias[i] = p.bias && e0 + i < p.E ? p.bias[e0 + i] : 0.0f;
+      number |= uint64_t((e0 + i) / size - first) << (4 * i);
+    }
+    const int lanes = size / PER;
+    span = size % PER == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  }
+};
+
+// choose_grouped in FP32, as far as that can tell the experts and groups apart; false,
+// and nothing written, when it cannot.  A score is off by less than 2^-19.5 of the
+// token's largest (`reach`, for sigmoid 1): exp within 2 steps, its argument rounded
+// once (x e^x < 0.37), sums of 16 and 6 terms, a quotient.  So sums with the bias that
+// are 2^-17 (reach + |c|) apart stand in their true order, and groups' scores twice as
+// far apart.  Of 32768 tokens x 256 experts some 0.3 % are nearer; scores in 64 bits for
+// all of them took 160 us of 186.
+template <int PER>
+__device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)[PER],
+                                   const Groups<PER>& groups, int32_t* ids, float* scratch) {
+  const int lane = threadIdx.x & 63;
+  const float none = -__builtin_inff();
+  auto in_order = [] {  // a wave's LDS accesses are done in order: keep theirs
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  float c[PER], most = 0.0f, total = 1.0f, reach = 1.0f;
+  if (p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float x = exp_of(-fabsf(v[i]));
+      c[i] = (v[i] > 0.0f ? 1.0f : x) * __builtin_amdgcn_rcpf(1.0f + x);
+    }
+  } else {
+    most = v[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) most = fmaxf(most, v[i]);
+    most = wave_fmax(most);
+    total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      c[i] = v[i] == none ? 0.0f : exp_of(v[i] - most);
+      total += c[i];
+    }
+    total = wave_sum(total);
+    reach = 1.0f / total;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] *= reach;
+  }
+  bool odd = false;  // NaN or infinities to compare
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] += groups.bias[i];
+    if (v[i] == none) c[i] = none;
+    odd = odd || !(c[i] <= 0x1p126f);
+  }
+  if (__ballot(odd)) return false;
+
+  uint64_t allowed = ~0ull;
+  if (p.groups > 1) {
+    // Without a bias the best scores are those of the best logits.
+    const bool by_logit = !p.bias && p.group_best == 1;
+    // Every lane of a block of `span` lanes gets its group's score.
+    int span = groups.span, group = groups.first;
+    float one = none, two = none;
+    auto add = [&](float x) {
+      two = fmaxf(two, fminf(one, x));
+      one = fmaxf(one, x);
+    };
+    if (span) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) add(by_logit ? v[i] : c[i]);
+    } else {  // by way of LDS: the lanes share out among as many groups as there can be
+      span = 64;
+      while (span * p.groups > 64) span >>= 1;
+      group = lane / span;
+      in_order();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) scratch[lane * PER + i] = by_logit ? v[i] : c[i];
+      in_order();
+      if (group < p.groups)
+        for (int i = lane & (span - 1); i < groups.size; i += span)
+          add(scratch[group * groups.size + i]);
+    }
+    join_best<1>(one, two, span);
+    const bool mine = group < p.groups;
+    float score = p.group_best == 2 && two != none ? one + two : one;
+    if (!mine) score = none;
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const float s =
+          __int_as_float(__builtin_amdgcn_readlane(__float_as_int(score), g * span));
+      rank += s > score || (s == score && g < group);
+    }
+    const bool is = mine && score != none;
+    // The last group that is taken and the first that is not.
+    const uint64_t last = __ballot(is && rank == p.top_groups - 1);
+    const uint64_t next = __ballot(is && rank == p.top_groups);
+    if (last && next && !by_logit) {
+      const float a = __int_as_float(__builtin_amdgcn_readlane(
+          __float_as_int(score), __ffsll((unsigned long long)last) - 1));
+      const float b = __int_as_float(__builtin_amdgcn_readlane(
+          __float_as_int(score), __ffsll((unsigned long long)next) - 1));
+      if (!(a - b > 0x1p-16f * (reach + fabsf(a)))) return false;
+    }
+    const uint64_t lanes = __ballot(is && rank < p.top_groups);
+    if (groups.span) {
+      allowed = lanes >> lane & 1 ? ~0ull : 0;  // a lane is in one group
+    } else {
+      allowed = 0;
+      for (int g = 0; g < p.groups; ++g) allowed |= (lanes >> (g * span) & 1) << g;
+    }
+  }
+  float by[PER];
+  uint64_t number = groups.number;
+  asm volatile("" : "+v"(number));  // not PER numbers kept over the tokens
+  allowed >>= groups.span || p.groups == 1 ? 0 : groups.first & 63;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const bool ok = allowed >> (number >> (4 * i) & 15) & 1;
+    by[i] = ok && c[i] != none ? (p.bias ? c[i] : v[i]) : none;
+  }
+  if (p.bias) {  // the slots' logits are looked up there: of their keys only the sums are known
+    in_order();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) scratch[lane * PER + i] = v[i];
+    in_order();
+  }
+  int mine;
+  uint32_t mine_key;
+  uint32_t rest = take_largest<PER>(by, p.k, mine, mine_key);
+  const int n = __popcll(__ballot(mine >= 0));
+  float l = of_key(mine_key);  // the slot's logit
+  if (p.bias) {
+    const float sum = l;
+    if (mine >= 0) l = scratch[mine];
+    // Each slot's sum against the next one's, the last one's against what is left.
+    rest = wave_max(rest);
+    uint32_t below = uint32_t(__builtin_amdgcn_update_dpp(0, int(mine_key), 0x101, 0xf, 0xf, true));
+    if (lane == n - 1) below = rest;
+    const bool near = lane < n && below > kNoKey &&
+                      !(sum - of_key(below) > 0x1p-17f * (reach + fabsf(sum)));
+    if (__ballot(near)) {
+      // Of the same logit and bias: a tie in any number of bits.
+      const int e = __builtin_amdgcn_update_dpp(-1, mine, 0x101, 0xf, 0xf, false);
+      bool same = false;
+      if (near && lane < n - 1 && e >= 0)
+        same = scratch[e] == l && p.bias[e] == p.bias[mine];
+      if (__ballot(near && !same)) return false;
+    }
+  }
+  float s = 0.0f;
+  if (mine >= 0) {
+    const float x = exp_of(p.sigmoid ? -fabsf(l) : l - most);
+    s = !p.sigmoid ? x : (l > 0.0f ? 1.0f : x) / (1.0f + x);
+  }
+  if (p.renorm) {
+    total = wave_sum(s);
+    if (n && !(total > 0x1p-80f)) return false;
+  }
+  if (lane < p.k) {
+    const int64_t slot = int64_t(t) * p.k + lane;
+    p.experts[slot] = mine;
+    p.weights[slot] = mine >= 0 ? p.scale * s / total : 0.0f;
+    ids[lane] = mine;
+  }
+  return true;
+}
+
+template <int PER, bool GROUPED>
+struct Chooser {
+  __device__ void init(const RouteParams&) {}
+  __device__ void operator()(const RouteParams& p, int t, const float (&v)[PER], int32_t* ids,
+                             float*) const {
+    choose<PER>(p, t, v, ids);
+  }
+};
+template <int PER>
+struct Chooser<PER, true> {
+  Groups<PER> groups;
+  __device__ void init(const RouteParams& p) { groups.init(p); }
+  __device__ void operator()(const RouteParams& p, int t, const float (&v)[PER], int32_t* ids,
+                             float* scratch) const {
+    if (!choose_near<PER>(p, t, v, groups, ids, scratch)) choose_grouped(p, t, ids, scratch);
+  }
+};
 
 // ------------------------------------------------------------------ the slots' order
 
@@ -453,12 +676,15 @@ __global__ __launch_bounds__(kThreads) void route_small(const RouteParams p) {
   __shared__ int32_t ids[kRouteSmall];
   __shared__ uint16_t hist[kWaves][kMaxE];
   __shared__ int32_t run[kMaxE];
+  __shared__ __attribute__((aligned(16))) float scratch[GROUPED ? kWaves : 1][GROUPED ? 128 * PER : 1];
   const int tid = threadIdx.x, wave = tid >> 6;
   const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
+  Chooser<PER, GROUPED> chooser;
+  chooser.init(p);
   for (int t = wave; t < p.tokens; t += kWaves) {
     Row<PER> row;
     row.load(p.logits, t * p.stride, p.E, p.dtype, vec);
-    choose_token<PER, GROUPED>(p, t, row.v, ids + t * p.k);
+    chooser(p, t, row.v, ids + t * p.k, scratch[GROUPED ? wave : 0]);
   }
   for (int i = tid; i < p.E; i += kThreads) run[i] = 0;
   __syncthreads();
@@ -489,8 +715,11 @@ __global__ __launch_bounds__(kThreads) void route_choose(const RouteParams p, in
   __shared__ int32_t ids[kRouteMost * 16];
   __shared__ uint16_t hist[kWaves][kMaxE];
   __shared__ int32_t run[kMaxE];
+  __shared__ __attribute__((aligned(16))) float scratch[GROUPED ? kWaves : 1][GROUPED ? 128 * PER : 1];
   const int tid = threadIdx.x, wave = tid >> 6;
   const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
+  Chooser<PER, GROUPED> chooser;
+  chooser.init(p);
   for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int t0 = b * p.per_block;
     const int nt = p.tokens - t0 < p.per_block ? p.tokens - t0 : p.per_block;
@@ -500,7 +729,7 @@ __global__ __launch_bounds__(kThreads) void route_choose(const RouteParams p, in
     for (int t = wave; t < nt; t += kWaves) {
       row = next;
       if (t + kWaves < nt) next.load(p.logits, (t0 + t + kWaves) * p.stride, p.E, p.dtype, vec);
-      choose_token<PER, GROUPED>(p, t0 + t, row.v, ids + t * p.k);
+      chooser(p, t0 + t, row.v, ids + t * p.k, scratch[GROUPED ? wave : 0]);
     }
     for (int i = tid; i < p.E; i += kThreads) run[i] = 0;
     __syncthreads();
