@@ -108,7 +108,9 @@ struct Row {
   float v[PER];
 
   __device__ void load(const void* p, int64_t at, int E, int dtype, bool vec) {
-    const int e0 = (threadIdx.x & 63) * PER;
+    load_from((threadIdx.x & 63) * PER, p, at, E, dtype, vec);
+  }
+  __device__ void load_from(int e0, const void* p, int64_t at, int E, int dtype, bool vec) {
     if (PER > 1 && vec) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = -__builtin_inff();
@@ -415,39 +417,53 @@ __device__ inline void join_best(float& one, float& two, int span) {
   }
 }
 
-// What a wave keeps over its tokens: the bias of its experts, and how groups lie in it.
-template <int PER>
+// f(0) .. f(15), each number as a type.
+template <int N = 0, class F>
+__device__ inline void each16(F f) {
+  f(std::integral_constant<int, N>{});
+  if constexpr (N < 15) each16<N + 1>(f);
+}
+
+// What a lane keeps over its tokens, of which each has LANES: how the groups lie among
+// its experts.
+template <int PER, int LANES>
 struct Groups {
-  float bias[PER];
   uint64_t number = 0;   // the PER experts' groups after the first's, 4 bits each
   int first;             // group of the lane's first expert
   int span;              // lanes of a group, when they hold nothing else; else 0
   int size;
 
   __device__ void init(const RouteParams& p) {
-    const int lane = threadIdx.x & 63, e0 = lane * PER;
+    const int e0 = (threadIdx.x & (LANES - 1)) * PER;
     size = p.E / p.groups;
     first = e0 / size;
+    int in_group = e0 - first * size, after = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      bias[i] = p.bias && e0 + i < p.E ? p.bias[e0 + i] : 0.0f;
-      number |= uint64_t((e0 + i) / size - first) << (4 * i);
+      number |= uint64_t(after) << (4 * i);
+      if (++in_group == size) in_group = 0, ++after;
     }
     const int lanes = size / PER;
     span = size % PER == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
   }
 };
 
+// How far apart sums of score and bias have to be, in FP32, to stand in their true
+// order, as a part of `reach`, the token's largest score (sigmoid: 1), and of the sum
+// itself; groups' scores, of two, twice as far.  One step is 2^-23 of a value.  exp is
+// within 1.5 steps.  Sigmoid: past 1/2 half of that, 1 + x within half a step and its
+// inverse within one, 2^-22; below 1/2 a product's half step more, 2^-21.3 of less than
+// 1/2; with the sum's rounding two are off by less than 2 (2^-22 + 2^-24).  Softmax: the
+// argument's rounding (x e^x < 0.37) and the product with the inverse, 2^-21.9 each, and
+// what all have in common, the sum of 16 and 6 terms, 22 half steps of their distance.
+__device__ inline float apart(const RouteParams& p) { return p.sigmoid ? 0x1p-20f : 0x1p-18f; }
+
 // choose_grouped in FP32, as far as that can tell the experts and groups apart; false,
-// and nothing written, when it cannot.  A score is off by less than 2^-19.5 of the
-// token's largest (`reach`, for sigmoid 1): exp within 2 steps, its argument rounded
-// once (x e^x < 0.37), sums of 16 and 6 terms, a quotient.  So sums with the bias that
-// are 2^-17 (reach + |c|) apart stand in their true order, and groups' scores twice as
-// far apart.  Of 32768 tokens x 256 experts some 0.3 % are nearer; scores in 64 bits for
-// all of them took 160 us of 186.
+// and nothing written, when it cannot.
 template <int PER>
 __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)[PER],
-                                   const Groups<PER>& groups, int32_t* ids, float* scratch) {
+                                   const Groups<PER, 64>& groups, const float* bias,
+                                   int32_t* ids, float* scratch) {
   const int lane = threadIdx.x & 63;
   const float none = -__builtin_inff();
   auto in_order = [] {  // a wave's LDS accesses are done in order: keep theirs
@@ -480,7 +496,7 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
   bool odd = false;  // NaN or infinities to compare
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    c[i] += groups.bias[i];
+    c[i] += bias[lane * PER + i];
     if (v[i] == none) c[i] = none;
     odd = odd || !(c[i] <= 0x1p126f);
   }
@@ -493,8 +509,8 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
     // Every lane of a block of `span` lanes gets its group's score.
     int span = groups.span, group = groups.first;
     float one = none, two = none;
-    auto add = [&](float x) {
-      two = fmaxf(two, fminf(one, x));
+    auto add = [&](float x) {  // the middle one of three is the second of all
+      two = __builtin_amdgcn_fmed3f(one, two, x);
       one = fmaxf(one, x);
     };
     if (span) {
@@ -531,7 +547,7 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
           __float_as_int(score), __ffsll((unsigned long long)last) - 1));
       const float b = __int_as_float(__builtin_amdgcn_readlane(
           __float_as_int(score), __ffsll((unsigned long long)next) - 1));
-      if (!(a - b > 0x1p-16f * (reach + fabsf(a)))) return false;
+      if (!(a - b > 2 * apart(p) * (reach + fabsf(a)))) return false;
     }
     const uint64_t lanes = __ballot(is && rank < p.top_groups);
     if (groups.span) {
@@ -569,7 +585,7 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
     uint32_t below = uint32_t(__builtin_amdgcn_update_dpp(0, int(mine_key), 0x101, 0xf, 0xf, true));
     if (lane == n - 1) below = rest;
     const bool near = lane < n && below > kNoKey &&
-                      !(sum - of_key(below) > 0x1p-17f * (reach + fabsf(sum)));
+                      !(sum - of_key(below) > apart(p) * (reach + fabsf(sum)));
     if (__ballot(near)) {
       // Of the same logit and bias: a tie in any number of bits.
       const int e = __builtin_amdgcn_update_dpp(-1, mine, 0x101, 0xf, 0xf, false);
@@ -597,23 +613,273 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
   return true;
 }
 
-template <int PER, bool GROUPED>
-struct Chooser {
-  __device__ void init(const RouteParams&) {}
-  __device__ void operator()(const RouteParams& p, int t, const float (&v)[PER], int32_t* ids,
-                             float*) const {
-    choose<PER>(p, t, v, ids);
-  }
-};
+// ---- four tokens by a wave, 16 lanes (a row of lane moves) to each
+
+// f over each row of 16, in all of its lanes.
+template <class F>
+__device__ inline float row_all(float v, F f) {
+  v = f(v, other_lanes<1>(v));
+  v = f(v, other_lanes<2>(v));
+  v = f(v, other_lanes<4>(v));
+  return f(v, other_lanes<8>(v));
+}
+__device__ inline float row_fmax(float v) {
+  return row_all(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ inline float row_sum(float v) {
+  return row_all(v, [](float a, float b) { return a + b; });
+}
+__device__ inline uint32_t row_max(uint32_t v) {
+  const auto f = [](float a, float b) {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    return __uint_as_float(x > y ? x : y);
+  };
+  return __float_as_uint(row_all(__uint_as_float(v), f));
+}
+// The bits of a row's lanes.
+__device__ inline uint32_t row_ballot(bool v) {
+  const uint64_t all = __ballot(v);
+  const uint32_t half = threadIdx.x & 32 ? uint32_t(all >> 32) : uint32_t(all);
+  return half >> (threadIdx.x & 16) & 0xffff;
+}
+
+// f(a, b) for the pairs of a sorting network of N places (a power of two), by merging
+// sorted halves of even and odd places.
+template <int N, class F>
+__device__ inline void sorting_network(F f) {
+#pragma unroll
+  for (int len = 1; len < N; len *= 2)
+#pragma unroll
+    for (int d = len; d > 0; d /= 2)
+#pragma unroll
+      for (int j = d % len; j + d < N; j += 2 * d)
+#pragma unroll
+        for (int i = 0; i < d && i + j + d < N; ++i)
+          if ((i + j) / (2 * len) == (i + j + d) / (2 * len)) f(i + j, i + j + d);
+}
+
+// choose_near for a token in each row: 375 vector instructions per token of 256 experts
+// for the wave's 700 (32768 of them: 66 -> 39 us), the reductions being four moves for
+// four tokens.  `ids` and `scratch` are the row's.  False in the lanes of a row whose token has to go by
+// 64 bits.
 template <int PER>
-struct Chooser<PER, true> {
-  Groups<PER> groups;
-  __device__ void init(const RouteParams& p) { groups.init(p); }
-  __device__ void operator()(const RouteParams& p, int t, const float (&v)[PER], int32_t* ids,
-                             float* scratch) const {
-    if (!choose_near<PER>(p, t, v, groups, ids, scratch)) choose_grouped(p, t, ids, scratch);
+__device__ inline bool choose_rows(const RouteParams& p, int64_t t, bool there,
+                                   const float (&v)[PER], const Groups<PER, 16>& groups,
+                                   const float* bias, int32_t* ids, float* scratch) {
+  const int q = threadIdx.x & 15;
+  const float none = -__builtin_inff();
+  auto in_order = [] {  // a wave's LDS accesses are done in order: keep theirs
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  float c[PER], most = 0.0f, total = 1.0f, reach = 1.0f;
+  if (p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float x = exp_of(-fabsf(v[i]));
+      c[i] = (v[i] > 0.0f ? 1.0f : x) * __builtin_amdgcn_rcpf(1.0f + x);
+    }
+  } else {
+    most = v[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) most = fmaxf(most, v[i]);
+    most = row_fmax(most);
+    total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      c[i] = v[i] == none ? 0.0f : exp_of(v[i] - most);
+      total += c[i];
+    }
+    total = row_sum(total);
+    reach = 1.0f / total;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] *= reach;
   }
-};
+  bool slow = false;  // NaN or infinities to compare, or values too near each other
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] += bias[q * PER + i];
+    if (v[i] == none) c[i] = none;
+    slow = slow || !(c[i] <= 0x1p126f);
+  }
+
+  uint32_t allowed = 0xffff;  // by lanes: a group's are its `span` from group * span on
+  int span = groups.span;
+  if (p.groups > 1) {
+    const bool by_logit = !p.bias && p.group_best == 1;
+    int group = groups.first;
+    float one = none, two = none;
+    auto add = [&](float x) {  // the middle one of three is the second of all
+      two = __builtin_amdgcn_fmed3f(one, two, x);
+      one = fmaxf(one, x);
+    };
+    if (span) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) add(by_logit ? v[i] : c[i]);
+    } else {
+      span = 16;
+      while (span * p.groups > 16) span >>= 1;
+      group = q / span;
+      in_order();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) scratch[q * PER + i] = by_logit ? v[i] : c[i];
+      in_order();
+      if (group < p.groups)
+        for (int i = q & (span - 1); i < groups.size; i += span)
+          add(scratch[group * groups.size + i]);
+    }
+    join_best<1>(one, two, span);
+    float score = p.group_best == 2 && two != none ? one + two : one;
+    if (group >= p.groups) score = none;
+    int above = 0;  // lanes of groups before this one
+    each16([&](auto n) {
+      const float s = __int_as_float(__builtin_amdgcn_update_dpp(
+          0, __float_as_int(score), 0x150 + decltype(n)::value, 0xf, 0xf, true));
+      above += s > score || (s == score && decltype(n)::value < group * span);
+    });
+    const bool is = score != none;
+    // The last group that is taken and the first that is not.
+    const float a = row_fmax(is && above == (p.top_groups - 1) * span ? score : none);
+    const float b = row_fmax(is && above == p.top_groups * span ? score : none);
+    if (!by_logit && b != none) slow = slow || !(a - b > 2 * apart(p) * (reach + fabsf(a)));
+    allowed = row_ballot(is && above < p.top_groups * span);
+  }
+  // A bit for each of the lane's experts whose group is taken.
+  uint32_t taken = allowed >> (groups.first * span & 15) & 1 ? 0xffff : 0;
+  if (p.groups > 1 && !groups.span) {
+    uint64_t number = groups.number;
+    asm volatile("" : "+v"(number));  // not PER numbers kept over the tokens
+    taken = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int g = groups.first + int(number >> (4 * i) & 15);
+      taken |= (allowed >> (g * span & 15) & 1) << i;
+    }
+  }
+  // The values' keys and, below them, places, the first of equal ones on top: as the
+  // bits of positive doubles, which have a maximum and a minimum of one instruction.
+  double key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const float by = (taken >> i & 1) && c[i] != none ? (p.bias ? c[i] : v[i]) : none;
+    key[i] = __longlong_as_double(int64_t(key_of(by)) << 30 | (PER - 1 - i));
+  }
+  const auto key_bits = [](double k) { return uint64_t(__double_as_longlong(k)); };
+  if (p.bias) {  // the slots' logits are looked up there: of their keys only the sums are known
+    in_order();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) scratch[q * PER + i] = v[i];
+    in_order();
+  }
+  sorting_network<PER>([&](int a, int b) {
+    double hi, lo;  // in asm: the compiler would first make quiet what it takes for a NaN
+    asm("v_max_f64 %0, %2, %3\n\tv_min_f64 %1, %2, %3"
+        : "=&v"(hi), "=&v"(lo)
+        : "v"(key[a]), "v"(key[b]));
+    key[a] = hi, key[b] = lo;
+  });
+  // Lane j keeps slot j's key, its expert goes to ids.
+  uint32_t mine_key = 0;
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t top = uint32_t(key_bits(key[0]) >> 30), m = row_max(top);
+    const bool some = m > kNoKey;
+    if (!__ballot(some)) break;
+    if (q == j && some) mine_key = m;
+    const uint32_t has = row_ballot(top == m);
+    if (some && (has & ((2u << q) - 1)) == 1u << q) {  // the first lane of them
+      if (there) ids[j] = q * PER + PER - 1 - int(uint32_t(key_bits(key[0])) & 15);
+#pragma unroll
+      for (int i = 0; i + 1 < PER; ++i) key[i] = key[i + 1];
+      key[PER - 1] = 0.0;
+    }
+  }
+  const int n = __popc(row_ballot(mine_key > kNoKey));
+  in_order();
+  const int mine = there && q < n ? ids[q] : -1;
+  float l = of_key(mine_key);  // the slot's logit
+  if (p.bias) {
+    const float sum = l;
+    if (mine >= 0) l = scratch[mine];
+    // Each slot's sum against the next one's, the last one's against what is left.
+    const uint32_t rest = row_max(uint32_t(key_bits(key[0]) >> 30));
+    uint32_t below = uint32_t(__builtin_amdgcn_update_dpp(0, int(mine_key), 0x101, 0xf, 0xf, true));
+    if (q == n - 1) below = rest;
+    const bool near = q < n && below > kNoKey &&
+                      !(sum - of_key(below) > apart(p) * (reach + fabsf(sum)));
+    if (__ballot(near)) {
+      // Of the same logit and bias: a tie in any number of bits.
+      const int e = __builtin_amdgcn_update_dpp(-1, mine, 0x101, 0xf, 0xf, false);
+      bool same = false;
+      if (near && q < n - 1 && e >= 0 && mine >= 0)
+        same = scratch[e] == l && p.bias[e] == p.bias[mine];
+      slow = slow || (near && !same);
+    }
+  }
+  float s = 0.0f;
+  if (q < n) {
+    const float x = exp_of(p.sigmoid ? -fabsf(l) : l - most);
+    s = !p.sigmoid ? x : (l > 0.0f ? 1.0f : x) / (1.0f + x);
+  }
+  if (p.renorm) {
+    total = row_sum(s);
+    slow = slow || (n && !(total > 0x1p-80f));
+  }
+  const bool done = row_ballot(slow) == 0;
+  if (there && done && q < p.k) {
+    p.experts[t * p.k + q] = mine;
+    p.weights[t * p.k + q] = mine >= 0 ? p.scale * s / total : 0.0f;
+    ids[q] = mine;
+  }
+  return done;
+}
+
+// The bias to LDS, zeros past its end and where there is none.
+__device__ inline void put_bias(const RouteParams& p, float* bias, int n) {
+  for (int i = threadIdx.x; i < n; i += kThreads) bias[i] = p.bias && i < p.E ? p.bias[i] : 0.0f;
+  __syncthreads();
+}
+
+// How a workgroup's waves share out its tokens t0 .. t0 + n.  ROWS: four to a wave.
+template <int PER, bool GROUPED, bool ROWS>
+__device__ inline void choose_all(const RouteParams& p, int t0, int n, const float* bias,
+                                  int32_t* ids, float* scratch) {
+  const int wave = threadIdx.x >> 6;
+  const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
+  if constexpr (ROWS) {
+    const int row = threadIdx.x >> 4 & 3, e0 = (threadIdx.x & 15) * PER;
+    Groups<PER, 16> groups;
+    groups.init(p);
+    // Registers are for more waves, not for the next tokens' logits.
+    for (int first = wave * 4; first < n; first += kWaves * 4) {
+      const int t = first + row;
+      Row<PER> logits;  // -inf for a row without a token
+      logits.load_from(e0, p.logits, int64_t(t0 + t) * p.stride, t < n ? p.E : 0, p.dtype, vec);
+      const bool done = choose_rows<PER>(p, t0 + t, t < n, logits.v, groups, bias,
+                                         ids + t * p.k, scratch + row * 16 * PER);
+      const uint64_t left = __ballot(!done);
+      for (int r = 0; r < 4; ++r)
+        if (first + r < n && left >> (r * 16) & 1)
+          choose_grouped(p, t0 + first + r, ids + (first + r) * p.k, scratch);
+    }
+  } else {
+    Groups<GROUPED ? PER : 1, 64> groups;
+    if constexpr (GROUPED) groups.init(p);
+    // The next token's logits are on their way while one is chosen from.
+    Row<PER> row, next;
+    if (wave < n) next.load(p.logits, int64_t(t0 + wave) * p.stride, p.E, p.dtype, vec);
+    for (int t = wave; t < n; t += kWaves) {
+      row = next;
+      if (t + kWaves < n)
+        next.load(p.logits, int64_t(t0 + t + kWaves) * p.stride, p.E, p.dtype, vec);
+      if constexpr (GROUPED) {
+        if (!choose_near<PER>(p, t0 + t, row.v, groups, bias, ids + t * p.k, scratch))
+          choose_grouped(p, t0 + t, ids + t * p.k, scratch);
+      } else {
+        choose<PER>(p, t0 + t, row.v, ids + t * p.k);
+      }
+    }
+  }
+}
 
 // ------------------------------------------------------------------ the slots' order
 
@@ -671,21 +937,16 @@ __device__ inline int first_rows(int32_t* counts, int E) {
   return all;
 }
 
-template <int PER, bool GROUPED>
+template <int PER, bool GROUPED, bool ROWS>
 __global__ __launch_bounds__(kThreads) void route_small(const RouteParams p) {
   __shared__ int32_t ids[kRouteSmall];
   __shared__ uint16_t hist[kWaves][kMaxE];
   __shared__ int32_t run[kMaxE];
-  __shared__ __attribute__((aligned(16))) float scratch[GROUPED ? kWaves : 1][GROUPED ? 128 * PER : 1];
+  __shared__ __attribute__((aligned(16))) float scratch[GROUPED ? kWaves : 1][GROUPED ? (ROWS ? 64 : 128) * PER : 1];
+  __shared__ __attribute__((aligned(16))) float bias[GROUPED ? (ROWS ? 16 : 64) * PER : 1];
   const int tid = threadIdx.x, wave = tid >> 6;
-  const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
-  Chooser<PER, GROUPED> chooser;
-  chooser.init(p);
-  for (int t = wave; t < p.tokens; t += kWaves) {
-    Row<PER> row;
-    row.load(p.logits, t * p.stride, p.E, p.dtype, vec);
-    chooser(p, t, row.v, ids + t * p.k, scratch[GROUPED ? wave : 0]);
-  }
+  if constexpr (GROUPED) put_bias(p, bias, (ROWS ? 16 : 64) * PER);
+  choose_all<PER, GROUPED, ROWS>(p, 0, p.tokens, bias, ids, scratch[GROUPED ? wave : 0]);
   for (int i = tid; i < p.E; i += kThreads) run[i] = 0;
   __syncthreads();
   const int n = p.tokens * p.k;
@@ -710,27 +971,19 @@ __global__ __launch_bounds__(kThreads) void route_small(const RouteParams p) {
 
 // Choose: p.per_block tokens; the slots' ranks in the block go to place, the
 // block's counts to hist[e][block].
-template <int PER, bool GROUPED>
-__global__ __launch_bounds__(kThreads) void route_choose(const RouteParams p, int blocks) {
+template <int PER, bool GROUPED, bool ROWS>
+__global__ __launch_bounds__(kThreads, ROWS ? 4 : 1) void route_choose(const RouteParams p, int blocks) {
   __shared__ int32_t ids[kRouteMost * 16];
   __shared__ uint16_t hist[kWaves][kMaxE];
   __shared__ int32_t run[kMaxE];
-  __shared__ __attribute__((aligned(16))) float scratch[GROUPED ? kWaves : 1][GROUPED ? 128 * PER : 1];
+  __shared__ __attribute__((aligned(16))) float scratch[GROUPED ? kWaves : 1][GROUPED ? (ROWS ? 64 : 128) * PER : 1];
+  __shared__ __attribute__((aligned(16))) float bias[GROUPED ? (ROWS ? 16 : 64) * PER : 1];
   const int tid = threadIdx.x, wave = tid >> 6;
-  const bool vec = row_pieces<PER>(p.logits, p.stride, p.E, p.dtype);
-  Chooser<PER, GROUPED> chooser;
-  chooser.init(p);
+  if constexpr (GROUPED) put_bias(p, bias, (ROWS ? 16 : 64) * PER);
   for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int t0 = b * p.per_block;
     const int nt = p.tokens - t0 < p.per_block ? p.tokens - t0 : p.per_block;
-    // The next token's logits are on their way while one is chosen from.
-    Row<PER> row, next;
-    if (wave < nt) next.load(p.logits, (t0 + wave) * p.stride, p.E, p.dtype, vec);
-    for (int t = wave; t < nt; t += kWaves) {
-      row = next;
-      if (t + kWaves < nt) next.load(p.logits, (t0 + t + kWaves) * p.stride, p.E, p.dtype, vec);
-      chooser(p, t0 + t, row.v, ids + t * p.k, scratch[GROUPED ? wave : 0]);
-    }
+    choose_all<PER, GROUPED, ROWS>(p, t0, nt, bias, ids, scratch[GROUPED ? wave : 0]);
     for (int i = tid; i < p.E; i += kThreads) run[i] = 0;
     __syncthreads();
     const int n = nt * p.k;
@@ -881,6 +1134,7 @@ __global__ __launch_bounds__(256) void route_grouped_back(const RouteBackParams 
     __builtin_amdgcn_wave_barrier();
   };
   const float inverse_scale = 1.0f / p.scale;
+  // (Loads of the next tokens' slots ahead were no faster: 15 us for 14, 32768 x 256.)
   for (int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); t < p.tokens; t += step) {
     int e = -1;
     float w = 0.0f, g = 0.0f, l = 0.0f;
@@ -957,20 +1211,15 @@ void with_per(int E, F f) {
 
 }  // namespace
 
-template <bool GROUPED>
+template <int PER, bool GROUPED, bool ROWS>
 static hipError_t launch_route_of(const RouteParams& p, hipStream_t stream) {
   if (route_is_small(p.tokens, p.E, p.k)) {
-    with_per(p.E, [&](auto per) {
-      route_small<decltype(per)::value, GROUPED><<<dim3(1), dim3(kThreads), 0, stream>>>(p);
-    });
+    route_small<PER, GROUPED, ROWS><<<dim3(1), dim3(kThreads), 0, stream>>>(p);
     return hipGetLastError();
   }
-  const int blocks = route_blocks(p.tokens);
+  const int blocks = (p.tokens + p.per_block - 1) / p.per_block;
   const int grid = blocks < 65536 ? blocks : 65536;
-  with_per(p.E, [&](auto per) {
-    route_choose<decltype(per)::value, GROUPED>
-        <<<dim3(grid), dim3(kThreads), 0, stream>>>(p, blocks);
-  });
+  route_choose<PER, GROUPED, ROWS><<<dim3(grid), dim3(kThreads), 0, stream>>>(p, blocks);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   route_scan<<<dim3(p.E), dim3(64), 0, stream>>>(p, blocks);
@@ -983,7 +1232,23 @@ static hipError_t launch_route_of(const RouteParams& p, hipStream_t stream) {
 hipError_t launch_route(RouteParams p, hipStream_t stream) {
   (void)hipGetLastError();
   p.per_block = route_per_block(p.tokens);
-  return p.groups ? launch_route_of<true>(p, stream) : launch_route_of<false>(p, stream);
+  hipError_t e = hipSuccess;
+  if (!p.groups) {
+    with_per(p.E, [&](auto per) {
+      e = launch_route_of<decltype(per)::value, false, false>(p, stream);
+    });
+  } else if (p.E <= 256 && p.groups <= 16) {
+    // Four tokens to a wave: every wave of a block has some.
+    if (p.per_block < kWaves * 4) p.per_block = kWaves * 4;
+    if (p.E <= 64) e = launch_route_of<4, true, true>(p, stream);
+    else if (p.E <= 128) e = launch_route_of<8, true, true>(p, stream);
+    else e = launch_route_of<16, true, true>(p, stream);
+  } else {
+    with_per(p.E, [&](auto per) {
+      e = launch_route_of<decltype(per)::value, true, false>(p, stream);
+    });
+  }
+  return e;
 }
 
 hipError_t launch_route_back(const RouteBackParams& p, hipStream_t stream) {
