@@ -324,23 +324,41 @@ __device__ inline uint32_t fp8_codes(float a, float b, float c, float d) {
   return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
 }
 
-// 8 values of a row of `cols` from column `col` on, zeros past its end.
+// 8 values of a row of `cols` from column `col` on, zeros past its end; kept as they
+// lie in memory until they are looked at, so that several are in flight.
 template <int DT, bool WHOLE>
-__device__ inline void load_eight(const typename Elem<DT>::type* x, int col, int cols,
-                                  float (&v)[8]) {
-  if constexpr (WHOLE && DT == A2AV_FP32) {
-    const auto lo = load_n<DT, 4, true>(x), hi = load_n<DT, 4, true>(x + 4);
+struct Eight {
+  using T = typename Elem<DT>::type;
+  static constexpr int kN = DT == A2AV_FP32 && WHOLE ? 4 : 8;
+  Pack<DT, kN, WHOLE> part[8 / kN];
+  __device__ void load(const T* x, int col, int cols) {
+    if (WHOLE || col + 8 <= cols) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[i + 4] = hi[i];
-  } else if (WHOLE || col + 8 <= cols) {
-    const auto w = load_n<DT, 8, WHOLE>(x);
+      for (int i = 0; i < 8 / kN; ++i) part[i] = load_n<DT, kN, WHOLE, true>(x + i * kN);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = w[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? Elem<DT>::up(x[i]) : 0.0f;
+      for (int i = 0; i < 8; ++i) part[i / kN].e[i % kN] = col + i < cols ? x[i] : T(0);
+    }
   }
-}
+  __device__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = part[i / kN][i % kN];
+  }
+};
+
+// The pieces of 8 values are numbered through, 16 to a block; a workgroup takes
+// kPieces * 256 of them in a row, each thread every 256th.
+constexpr int kPieces = 2;
+struct Piece8 {
+  int64_t row;
+  int b, col;
+  // Piece `first` + `i`, where `first` begins block b0 of row0.
+  __device__ static Piece8 at(int64_t row0, int b0, int i, int blocks) {
+    const uint32_t lb = uint32_t(b0) + uint32_t(i >> 4), rows = lb / uint32_t(blocks);
+    const int b = int(lb - rows * uint32_t(blocks));
+    return Piece8{row0 + rows, b, b * 128 + (i & 15) * 8};
+  }
+};
 
 __device__ inline uint32_t top_of(const float (&v)[8]) {
   uint32_t top = 0;  // magnitudes order like their bits
@@ -359,32 +377,51 @@ __device__ inline uint2 eight_codes(const float (&v)[8], int s) {
                fp8_codes(v[4] * up, v[5] * up, v[6] * up, v[7] * up)};
 }
 
-// Sixteen lanes per block of 128, 8 values each.
+// The largest over each row of 16 lanes, in all of them, by moves inside the row.
+__device__ inline uint32_t row_max(uint32_t v) {
+  const auto with = [](uint32_t a, int b) { return a > uint32_t(b) ? a : uint32_t(b); };
+  v = with(v, __builtin_amdgcn_update_dpp(0, int(v), 0xb1, 0xf, 0xf, true));   // its neighbour
+  v = with(v, __builtin_amdgcn_update_dpp(0, int(v), 0x4e, 0xf, 0xf, true));   // the next two
+  v = with(v, __builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xf, 0xf, true));  // half a row mirrored
+  return with(v, __builtin_amdgcn_update_dpp(0, int(v), 0x140, 0xf, 0xf, true));
+}
+
+// Sixteen lanes per block of 128, 8 values each, two pieces of each thread on their way
+// before the first is looked at (four: 2 us more).  16384 x 7168, bf16, to codes and
+// back: 110 us, 6.4 TB/s.  Codes stored past the caches are 8 us faster by themselves and
+// then 12 slower to read, and something always reads them next.
 template <int DT, bool WHOLE>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(const Fp8Params p) {
   using T = typename Elem<DT>::type;
   const int64_t all = p.rows * p.blocks * 16;
-  const int pitch = (p.blocks + 3) / 4 * 4;
-  for (int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x; q < all;
-       q += int64_t(gridDim.x) * 256) {
-    const int64_t block = q >> 4, row = block / p.blocks;
-    const int b = int(block - row * p.blocks);
-    const int col = b * 128 + int(q & 15) * 8;
-    float v[8];
-    load_eight<DT, WHOLE>(static_cast<const T*>(p.x) + row * p.stride + col, col, p.cols, v);
-    uint32_t top = top_of(v);
+  const int pitch = (p.blocks + 3) / 4 * 4, tid = threadIdx.x;
+  constexpr int kEach = kPieces * 256;
+  for (int64_t first = int64_t(blockIdx.x) * kEach; first < all; first += int64_t(gridDim.x) * kEach) {
+    const int64_t row0 = (first >> 4) / p.blocks;
+    const int b0 = int((first >> 4) - row0 * p.blocks);
+    const int left = int(all - first < kEach ? all - first : kEach);
+    Eight<DT, WHOLE> x[kPieces];
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1) {
-      const uint32_t u = __shfl_xor(top, d);
-      top = u > top ? u : top;
+    for (int u = 0; u < kPieces; ++u) {
+      const Piece8 c = Piece8::at(row0, b0, u * 256 + tid, p.blocks);
+      if (u * 256 + tid < left)
+        x[u].load(static_cast<const T*>(p.x) + c.row * p.stride + c.col, c.col, p.cols);
     }
-    const int s = fp8_scale(top);
-    reinterpret_cast<uint2*>(p.codes)[q] = eight_codes(v, s);
-    if ((q & 15) == 0) {
-      uint8_t* to = p.scales + row * pitch;
-      to[b] = uint8_t(s);
-      if (b == p.blocks - 1)
-        for (int i = p.blocks; i < pitch; ++i) to[i] = 0;
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int i = u * 256 + tid;
+      if (i >= left) break;  // 16 lanes have the same block
+      const Piece8 c = Piece8::at(row0, b0, i, p.blocks);
+      float v[8];
+      x[u].values(v);
+      const int s = fp8_scale(row_max(top_of(v)));
+      reinterpret_cast<uint2*>(p.codes)[first + i] = eight_codes(v, s);
+      if ((i & 15) == 0) {
+        uint8_t* to = p.scales + c.row * pitch;
+        to[c.b] = uint8_t(s);
+        if (c.b == p.blocks - 1)
+          for (int k = p.blocks; k < pitch; ++k) to[k] = 0;
+      }
     }
   }
 }
@@ -393,7 +430,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(const Fp8Params p) {
 template <int DT, bool WHOLE>
 __global__ __launch_bounds__(256) void fp8_weights_kernel(const Fp8Params p) {
   using T = typename Elem<DT>::type;
-  __shared__ uint32_t tops[4];
+  __shared__ uint32_t tops[16];
   const int tid = threadIdx.x, pitch = (p.blocks + 3) / 4 * 4;
   const int tall = (p.n + 127) / 128;
   const int64_t all = p.rows / p.n * tall * p.blocks;
@@ -402,37 +439,36 @@ __global__ __launch_bounds__(256) void fp8_weights_kernel(const Fp8Params p) {
     const int b = int(block - strip * p.blocks);
     const int n0 = int(strip - e * tall) * 128;
     const int col = b * 128 + (tid & 15) * 8;
-    float v[8][8];
-    uint32_t top = 0;
+    Eight<DT, WHOLE> x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int n = n0 + i * 16 + (tid >> 4);
+      if (n < p.n) x[i].load(static_cast<const T*>(p.x) + (e * p.n + n) * p.stride + col, col, p.cols);
+    }
+    uint32_t top = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-      if (n < p.n) {
-        const T* x = static_cast<const T*>(p.x) + (e * p.n + n) * p.stride + col;
-        load_eight<DT, WHOLE>(x, col, p.cols, v[i]);
-      }
-      const uint32_t u = top_of(v[i]);
+    for (int i = 0; i < 8; ++i) {
+      if (n0 + i * 16 + (tid >> 4) >= p.n) continue;
+      float v[8];
+      x[i].values(v);
+      const uint32_t u = top_of(v);
       top = u > top ? u : top;
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t u = __shfl_xor(top, d);
-      top = u > top ? u : top;
-    }
-    if ((tid & 63) == 0) tops[tid >> 6] = top;
+    top = row_max(top);
+    if ((tid & 15) == 0) tops[tid >> 4] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = tops[i] > top ? tops[i] : top;
+    for (int i = 0; i < 16; ++i) top = tops[i] > top ? tops[i] : top;
     __syncthreads();
     const int s = fp8_scale(top);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int n = n0 + i * 16 + (tid >> 4);
-      if (n < p.n)
-        reinterpret_cast<uint2*>(p.codes)[(e * p.n + n) * (p.blocks * 16) + b * 16 + (tid & 15)] =
-            eight_codes(v[i], s);
+      if (n >= p.n) continue;
+      float v[8];
+      x[i].values(v);
+      reinterpret_cast<uint2*>(p.codes)[(e * p.n + n) * (p.blocks * 16) + b * 16 + (tid & 15)] =
+          eight_codes(v, s);
     }
     if (tid == 0) {
       uint8_t* to = p.scales + strip * pitch;
@@ -447,41 +483,56 @@ template <int DT, bool WHOLE>
 __global__ __launch_bounds__(256) void fp8_values_kernel(const Fp8Params p) {
   using T = typename Elem<DT>::type;
   const int64_t all = p.rows * p.blocks * 16;
-  const int pitch = (p.blocks + 3) / 4 * 4;
-  for (int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x; q < all;
-       q += int64_t(gridDim.x) * 256) {
-    const int64_t block = q >> 4, row = block / p.blocks;
-    const int b = int(block - row * p.blocks);
-    const int col = b * 128 + int(q & 15) * 8;
-    int64_t strip = row;
-    if (p.n) {
-      const int64_t e = row / p.n;
-      strip = e * ((p.n + 127) / 128) + (row - e * p.n) / 128;
-    }
-    const uint2 codes = reinterpret_cast<const uint2*>(p.codes_in)[q];
-    const uint32_t s = p.scales_in[strip * pitch + b];
-    // 2^(s - 127); below the normal numbers for s = 0, NaN for s = 255.
-    const float step = __uint_as_float(s == 255 ? 0x7fc00000u : s ? s << 23 : 0x00400000u);
-    float v[8];
+  const int pitch = (p.blocks + 3) / 4 * 4, tid = threadIdx.x;
+  constexpr int kEach = kPieces * 256;
+  for (int64_t first = int64_t(blockIdx.x) * kEach; first < all; first += int64_t(gridDim.x) * kEach) {
+    const int64_t row0 = (first >> 4) / p.blocks;
+    const int b0 = int((first >> 4) - row0 * p.blocks);
+    const int left = int(all - first < kEach ? all - first : kEach);
+    uint2 codes[kPieces];
+    uint32_t scales[kPieces];
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const int w = int(i ? codes.y : codes.x);
-      v[i] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * step;
-      v[i + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * step;
-      v[i + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * step;
-      v[i + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * step;
+    for (int u = 0; u < kPieces; ++u) {
+      const int i = u * 256 + tid;
+      if (i >= left) continue;
+      const Piece8 c = Piece8::at(row0, b0, i, p.blocks);
+      int64_t strip = c.row;
+      if (p.n) {
+        const int64_t e = c.row / p.n;
+        strip = e * ((p.n + 127) / 128) + (c.row - e * p.n) / 128;
+      }
+      codes[u] = reinterpret_cast<const uint2*>(p.codes_in)[first + i];
+      scales[u] = p.scales_in[strip * pitch + c.b];
     }
-    T* x = static_cast<T*>(p.out) + row * p.stride + col;
-    if constexpr (WHOLE && DT == A2AV_FP32) {
-      const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-      store_n<DT, 4, true, true>(x, lo);
-      store_n<DT, 4, true, true>(x + 4, hi);
-    } else if (WHOLE || col + 8 <= p.cols) {
-      store_n<DT, 8, WHOLE, true>(x, v);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < p.cols) x[i] = Elem<DT>::down(v[i]);
+    for (int u = 0; u < kPieces; ++u) {
+      const int i = u * 256 + tid;
+      if (i >= left) break;
+      const Piece8 c = Piece8::at(row0, b0, i, p.blocks);
+      const uint32_t s = scales[u];
+      // 2^(s - 127); below the normal numbers for s = 0, NaN for s = 255.
+      const float step = __uint_as_float(s == 255 ? 0x7fc00000u : s ? s << 23 : 0x00400000u);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const int w = int(j ? codes[u].y : codes[u].x);
+        v[j] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * step;
+        v[j + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * step;
+        v[j + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * step;
+        v[j + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * step;
+      }
+      T* x = static_cast<T*>(p.out) + c.row * p.stride + c.col;
+      if constexpr (WHOLE && DT == A2AV_FP32) {
+        const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+        store_n<DT, 4, true, true>(x, lo);
+        store_n<DT, 4, true, true>(x + 4, hi);
+      } else if (WHOLE || c.col + 8 <= p.cols) {
+        store_n<DT, 8, WHOLE, true>(x, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c.col + j < p.cols) x[j] = Elem<DT>::down(v[j]);
+      }
     }
   }
 }
@@ -600,7 +651,7 @@ static bool whole_rows(const Fp8Params& p, const void* rows) {
 hipError_t launch_fp8_quantize(const Fp8Params& p, hipStream_t stream) {
   const bool whole = whole_rows(p, p.x);
   const int64_t want = p.n ? p.rows / p.n * ((p.n + 127) / 128) * p.blocks
-                           : (p.rows * p.blocks * 16 + 255) / 256;
+                           : (p.rows * p.blocks * 16 + kPieces * 256 - 1) / (kPieces * 256);
   const dim3 grid(uint32_t(want < (1 << 20) ? want : (1 << 20)));
   return with_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
@@ -617,7 +668,7 @@ hipError_t launch_fp8_quantize(const Fp8Params& p, hipStream_t stream) {
 
 hipError_t launch_fp8_dequantize(const Fp8Params& p, hipStream_t stream) {
   const bool whole = whole_rows(p, p.out);
-  const int64_t want = (p.rows * p.blocks * 16 + 255) / 256;
+  const int64_t want = (p.rows * p.blocks * 16 + kPieces * 256 - 1) / (kPieces * 256);
   const dim3 grid(uint32_t(want < (1 << 20) ? want : (1 << 20)));
   return with_dtype(p.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
