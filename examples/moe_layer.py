@@ -1,6 +1,6 @@
 """A mixture-of-experts layer on one MI355X, from logits to gradients.
 
-Two paths, as a program would run them:
+Four paths, as a program would run them:
 
 ``expert_parallel``  P virtual ranks with E / P experts each.  Every rank routes
     its tokens, the exchange gathers and delivers their rows, each rank
@@ -8,10 +8,15 @@ Two paths, as a program would run them:
     brings the rows back, and the weighted return makes tokens of them.
 ``training_step``    one rank, forward and backward: the gradients of the tokens,
     of both weights and of the router's logits.
+``expert_parallel_8``, ``training_step_8``  the same in 8 bits, with the router by
+    groups: a token goes to a few ranks only, a bias balances the experts, the
+    exchange carries 8-bit codes and their scales, and the products of both
+    directions run on them.  The weights' gradients stay in 16 bits.
 
-``python examples/moe_layer.py [--mx4]`` runs both, checks them against a dense
-float64 layer and prints the errors.  With ``--mx4`` the products of the first
-path run on 4-bit rows and weights, and the error is that of the format.
+``python examples/moe_layer.py [--mx4 | --fp8]`` runs the first two, or the last two,
+checks them against a dense float64 layer and prints the errors.  With ``--mx4`` the
+products of the first path run on 4-bit rows and weights.  In 4 and 8 bits the error
+is that of the format.
 """
 from __future__ import annotations
 
@@ -107,6 +112,95 @@ def training_step(x, logits, w1, w2, dout, k: int):
     return out, dx, dlogits, dw1, dw2
 
 
+def deliver(rows, lists, to_rank, most: int):
+    """rows [P, n, bytes] to the ranks that ``lists`` and ``to_rank`` (rows s -> d) name:
+    [P, most, bytes], a rank's rows by source."""
+    P, n, width = rows.shape
+    words = width // 4  # 32-bit words of a row
+    ex = a2av.Exchange(P, n * width, most * width, P)
+    received = torch.empty(P, most, width, dtype=rows.dtype, device=rows.device)
+    signal = torch.zeros(P, P, dtype=torch.int32, device=rows.device)
+    recv_counts = torch.empty(P, P, dtype=torch.int32, device=rows.device)
+    ex.run(rows.view(torch.uint8), received.view(torch.uint8), signal, to_rank * words, recv_counts,
+           P, a2av.FP32, index=lists, row_elems=words, check=True)
+    ex.close()
+    return received
+
+
+def expert_parallel_8(x, logits, bias, w1, w2, k: int, groups: int, top_groups: int,
+                      scale: float = 1.0):
+    """x [P, T, H] bf16, logits [P, T, E], bias [E], w1 [E, F, H], w2 [E, H, F]: the
+    layer's output [P, T, H] and the routes, products and dispatch in 8 bits."""
+    P, T, H = x.shape
+    E = logits.shape[2]
+    local = E // P
+    dev = x.device
+    routes = [moe.route_grouped(logits[s], k, bias=bias, groups=groups, top_groups=top_groups,
+                                scale=scale) for s in range(P)]
+    counts = torch.stack([r.counts for r in routes])
+    to_rank = counts.view(P, P, local).sum(2, dtype=torch.int32)
+    lists = torch.stack([r.order for r in routes])
+    most = P * T * k
+
+    # There: a row's codes, and its scales beside them.
+    codes, scales = moe.fp8_quantize(x.view(P * T, H))
+    got_codes = deliver(codes.view(P, T, -1), lists, to_rank, most)
+    got_scales = deliver(scales.view(P, T, -1), lists, to_rank, most)
+    weights = [moe.fp8_quantize_weights(w) for w in (w1, w2)]  # a program keeps these
+
+    out_rows = torch.empty(P, most, H, dtype=x.dtype, device=dev)
+    back_lists = torch.zeros(P, most, dtype=torch.int32, device=dev)
+    for d in range(P):
+        mine = counts[:, d * local:(d + 1) * local].contiguous()  # [source, expert of d]
+        n = int(mine.sum())
+        expert = torch.arange(local, device=dev).repeat(P).repeat_interleave(mine.view(-1).long())
+        by_expert = expert.sort(stable=True).indices.to(torch.int32)
+        per_expert = mine.sum(0, dtype=torch.int32)
+        (c1, s1), (c2, s2) = [[t[d * local:(d + 1) * local] for t in w] for w in weights]
+        h = moe.gmm_fp8(got_codes[d, :max(n, 1)], got_scales[d, :max(n, 1)], c1, s1, per_expert,
+                        index=by_expert, dtype=x.dtype, check=True)
+        out_rows[d, :n] = moe.gmm_fp8(*moe.fp8_quantize(silu(h)), c2, s2, per_expert,
+                                      dtype=x.dtype, check=True)
+        back_lists[d, by_expert.long()] = torch.arange(n, dtype=torch.int32, device=dev)
+
+    # Back, in 16 bits: what is added up for a token.
+    returned = deliver(out_rows.view(torch.uint8), back_lists, to_rank.t().contiguous(), T * k)
+    returned = returned.view(x.dtype)
+    out = torch.stack([moe.combine(returned[s], r.place, r.weights, check=True)
+                       for s, r in enumerate(routes)])
+    return out, routes
+
+
+def training_step_8(x, logits, bias, w1, w2, dout, k: int, groups: int, top_groups: int,
+                    scale: float = 1.0):
+    """x [T, H], logits [T, E], dout [T, H]: (out, dx, dlogits, dw1, dw2) and the route."""
+    H, F = x.shape[1], w1.shape[1]
+    r = moe.route_grouped(logits, k, bias=bias, groups=groups, top_groups=top_groups, scale=scale)
+    q1, q2 = moe.fp8_quantize_weights(w1), moe.fp8_quantize_weights(w2)
+    h = moe.gmm_fp8(*moe.fp8_quantize(x), *q1, r.counts, index=r.order, dtype=x.dtype)
+    a = silu(h)
+    y = moe.gmm_fp8(*moe.fp8_quantize(a), *q2, r.counts, dtype=x.dtype)
+    out = moe.combine(y, r.place, r.weights)
+
+    dy, dweights = moe.combine_backward(dout, y, r.place, r.weights)
+    dw2 = moe.gmm_dw(dy, a, r.counts)
+    da = moe.gmm_fp8_dx(*moe.fp8_quantize(dy), *q2, r.counts, cols=F, dtype=x.dtype)
+    s = torch.sigmoid(h.float())
+    dh = (da.float() * (s * (1 + h.float() * (1 - s)))).to(h.dtype)
+    dw1 = moe.gmm_dw(dh, x, r.counts, index=r.order)
+    dx = moe.combine(moe.gmm_fp8_dx(*moe.fp8_quantize(dh), *q1, r.counts, cols=H, dtype=x.dtype),
+                     r.place)
+    dlogits = moe.route_grouped_backward(logits, r.experts, r.weights, dweights, scale=scale)
+    return (out, dx, dlogits, dw1, dw2), r
+
+
+def dense_8(x, logits, w1, w2, experts, scale: float = 1.0):
+    """The layer in float64 with autograd, of these experts [.., k]."""
+    s = torch.sigmoid(logits) * torch.zeros_like(logits).scatter(-1, experts.long().cpu(), 1.0)
+    h = silu(torch.einsum("...h,efh->...ef", x, w1))
+    return torch.einsum("...ef,ehf,...e->...h", h, w2, scale * s / s.sum(-1, keepdim=True))
+
+
 def dense(x, logits, w1, w2, k: int, renormalize: bool):
     """The layer in float64 with autograd, every expert on every token."""
     p = torch.softmax(logits, -1)
@@ -135,18 +229,29 @@ def relative(a, b) -> float:
 
 def main() -> int:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
-    ap.add_argument("--mx4", action="store_true")
+    form = ap.add_mutually_exclusive_group()
+    form.add_argument("--mx4", action="store_true")
+    form.add_argument("--fp8", action="store_true")
     a = ap.parse_args()
     P, T, E, H, F, k = 4, 96, 8, 256, 512, 2
     x, logits, w1, w2, dout = inputs(P, T, E, H, F)
-    out = expert_parallel(x, logits, w1, w2, k, a.mx4)
     wide = [t.double().cpu() for t in (x, logits, w1, w2)]
-    print("expert parallel, %d ranks: relative error %.2g" % (P, relative(out, dense(*wide, k, True))))
-    got = training_step(x[0], logits[0], w1, w2, dout[0], k)
     leaves = [t.clone().requires_grad_() for t in (wide[0][0], wide[1][0], wide[2], wide[3])]
-    want = dense(*leaves, k, False)
-    grads = torch.autograd.grad(want, leaves, dout[0].double().cpu())
-    for name, g, w in zip(("out", "dx", "dlogits", "dw1", "dw2"), got, (want.detach(), *grads)):
+    if a.fp8:
+        bias = 0.01 * torch.arange(E, device=x.device).float()
+        args = (k, P, 2, 2.5)  # a group for each rank, of which a token goes to two
+        out, routes = expert_parallel_8(x, logits, bias, w1, w2, *args)
+        want = dense_8(*wide, torch.stack([r.experts for r in routes]), 2.5)
+        got, r = training_step_8(x[0], logits[0], bias, w1, w2, dout[0], *args)
+        loss = dense_8(*leaves, r.experts, 2.5)
+    else:
+        out = expert_parallel(x, logits, w1, w2, k, a.mx4)
+        want = dense(*wide, k, True)
+        got = training_step(x[0], logits[0], w1, w2, dout[0], k)
+        loss = dense(*leaves, k, False)
+    print("expert parallel, %d ranks: relative error %.2g" % (P, relative(out, want)))
+    grads = torch.autograd.grad(loss, leaves, dout[0].double().cpu())
+    for name, g, w in zip(("out", "dx", "dlogits", "dw1", "dw2"), got, (loss.detach(), *grads)):
         print("training step, %s: relative error %.2g" % (name, relative(g, w)))
     return 0
 
