@@ -586,17 +586,18 @@ def fp8_quantize(x, *, out=None, stream=None):
     C, S = _blocks(cols)
     if x.requires_grad or out is not None and out[0].requires_grad:
         _recorded()
-    dev = _device(x, *(out or ()))
+    dev = _device(x) if out is None else _device(x, *out)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
             return fp8_quantize(x, out=out)
     if out is None:
         out = (torch.empty(rows, C, dtype=E4M3, device=dev),
                torch.empty(rows, S, dtype=torch.uint8, device=dev))
-    st = lib().a2av_moe_fp8_quantize(p, stride, rows, cols, _DTYPE[x.dtype],
-                                     _whole(out[0], "codes", (rows, C), E4M3),
-                                     _whole(out[1], "scales", (rows, S), torch.uint8),
-                                     _stream(dev))
+        ptr = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        ptr = (_whole(out[0], "codes", (rows, C), E4M3),
+               _whole(out[1], "scales", (rows, S), torch.uint8))
+    st = lib().a2av_moe_fp8_quantize(p, stride, rows, cols, _DTYPE[x.dtype], *ptr, _stream(dev))
     a2av._raise(st, "a2av_moe_fp8_quantize")
     return out
 
