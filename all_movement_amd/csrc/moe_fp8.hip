@@ -231,6 +231,50 @@ __device__ inline void load_byte_to_lds(const uint8_t* base, uint32_t offset, ui
                : "memory");
 }
 
+// The sums as 16-bit rows straight from the registers.  A lane of group g holds the
+// columns 4 g .. 4 g + 3 of a fragment; of two fragments side by side, groups 2 h and
+// 2 h + 1 exchange halves, so that the even one has 8 columns of the first and the odd
+// one of the second: a store of 16 bytes per lane, 64 in a row.  No LDS, and so no
+// barrier: a 256 x 256 tile by way of LDS took the workgroup some 4 us more.
+template <int TM, int TN, int FM, int FN, class At>
+__device__ inline void store_halves(const GmmParams& p, const Tile& t, const float4v (&acc)[FM][FN],
+                                    int wm, int wn, At ready) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int col0 = wn * TN + (g & 1) * 16 + (g >> 1) * 8;
+  const bool wide = (p.out_stride & 7) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  uint16_t* const out = reinterpret_cast<uint16_t*>(p.out) + t.out_row0 * p.out_stride + t.c0;
+  const bool bf16 = p.out_type == A2AV_BF16;
+  auto two = [&](float a, float b) {
+    const uint32_t lo = bf16 ? __builtin_bit_cast(uint16_t, __bf16(a))
+                             : __builtin_bit_cast(uint16_t, _Float16(a));
+    const uint32_t hi = bf16 ? __builtin_bit_cast(uint16_t, __bf16(b))
+                             : __builtin_bit_cast(uint16_t, _Float16(b));
+    return lo | hi << 16;
+  };
+#pragma unroll
+  for (int a = 0; a < FM; ++a) {
+    ready(a);
+    const int r = wm * TM + a * 16 + l16;
+    uint16_t* const row = out + int64_t(r) * p.out_stride;
+#pragma unroll
+    for (int d = 0; d < FN; d += 2) {
+      const float4v u = acc[a][d], v = acc[a][d + 1];
+      const auto x = __builtin_amdgcn_permlane16_swap(two(u[0], u[1]), two(v[0], v[1]), false, false);
+      const auto y = __builtin_amdgcn_permlane16_swap(two(u[2], u[3]), two(v[2], v[3]), false, false);
+      const int4v piece = {int(x[0]), int(y[0]), int(x[1]), int(y[1])};
+      const int col = col0 + d * 16;
+      if (r >= t.rm || col >= t.cn) continue;
+      if (wide && col + 8 <= t.cn) {
+        *reinterpret_cast<int4v*>(row + col) = piece;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (col + i < t.cn) row[col + i] = uint16_t(uint32_t(piece[i / 2]) >> (16 * (i & 1)));
+      }
+    }
+  }
+}
+
 template <int BM, int BN, int NB>
 struct Pipe8 {
   static constexpr int NW = 4, kBuf = (BM + BN) * 128;
@@ -480,8 +524,9 @@ __device__ inline void fp8_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
   // The loads still in flight write to this workgroup's LDS; the last products have
   // to end before their sums are read.
   asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-  for (int a = 0; a < FM; ++a)
+  // The sums leave their registers row by row, where they are stored.
+  auto ready = [&](int a) {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int b = 0; b < FN; ++b) {
       if (a * FN + b >= kVector)
@@ -489,13 +534,12 @@ __device__ inline void fp8_tile(const GmmParams& p, const Tile& t, uint8_t* lds)
       else
         asm volatile("" : "+a"(acc[a][b]));
     }
+  };
   if (bad_row && p.status) *p.status = A2AV_ERR_INVALID_ARGS;
-  __syncthreads();  // everybody's reads and loads are done
-  constexpr int kPart = NB * kBuf / NW / 1024 * 1024;
   if (p.out_type == A2AV_FP32)
-    store_rows<MODE, TM, TN, FM, FN, 4, kPart>(p, t, acc, wm, wn, lds + wave * kPart);
+    store_tile<MODE, TM, TN, FM, FN>(p, t, acc, wm, wn, ready);
   else
-    store_rows<MODE, TM, TN, FM, FN, 2, kPart>(p, t, acc, wm, wn, lds + wave * kPart);
+    store_halves<TM, TN, FM, FN>(p, t, acc, wm, wn, ready);
 }
 
 // 256 x 256 tiles, one workgroup per CU.

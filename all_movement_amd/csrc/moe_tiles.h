@@ -204,9 +204,13 @@ __device__ inline uint16_t round16(float v, int type) {
 
 // A lane holds 4 columns (4g .. 4g + 3 of a fragment) of output row l16, stored
 // at once at any alignment of an element.
-template <int MODE, int TM, int TN, int FM, int FN>
+// ready(a) is called before the sums of fragment row a are looked at.
+struct Ready {
+  __device__ void operator()(int) const {}
+};
+template <int MODE, int TM, int TN, int FM, int FN, class At = Ready>
 __device__ inline void store_tile(const GmmParams& p, const Tile& t, const float4v (&acc)[FM][FN],
-                                  int wm, int wn) {
+                                  int wm, int wn, At ready = {}) {
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int64_t first = MODE == kGmmDw ? int64_t(t.span.e) * p.N + t.out_row0 : t.out_row0;
   struct __attribute__((packed, aligned(4))) Loose32 {
@@ -217,6 +221,7 @@ __device__ inline void store_tile(const GmmParams& p, const Tile& t, const float
   };
 #pragma unroll
   for (int a = 0; a < FM; ++a) {
+    ready(a);
     const int r = wm * TM + a * 16 + l16;
     if (r >= t.rm) continue;
 #pragma unroll
