@@ -200,12 +200,7 @@ def whole(shape, gen):
     return torch.randint(-8, 9, shape, generator=gen).float()
 
 
-@pytest.mark.parametrize("counts,N,K,tokens", [
-    ([1, 0, 5], 100, 4000, None), ([12] * 16, 256, 2048, 40), ([31, 17, 40, 2], 257, 1024, None),
-    ([260, 150, 390], 384, 1280, 333), ([1000, 24], 640, 900, None), ([513], 300, 7168, None),
-    ([2100, 5], 2300, 256, None), ([520, 300], 16640, 512, None),
-    ([64] * 5, 2304, 128, None), ([16], 4096, 8192, None)])
-def test_whole_numbers(counts, N, K, tokens):
+def whole_numbers(counts, N, K, tokens=None):
     """Every sum is a whole number below 2^24: equal to float64's."""
     gen = torch.Generator().manual_seed(N + K)
     E, rows = len(counts), sum(counts)
@@ -229,6 +224,25 @@ def test_whole_numbers(counts, N, K, tokens):
     assert torch.equal(y.cpu().double(), plain.gmm(x, w, c, index)[0])
     dx = moe.gmm_fp8_dx(yc, ys, wc, ws, c, cols=K, dtype=torch.float32, check=True)
     assert torch.equal(dx.cpu().double(), plain.gmm_dx(dy, w, c)[0])
+
+
+@pytest.mark.parametrize("counts,N,K,tokens", [
+    ([1, 0, 5], 100, 4000, None), ([12] * 16, 256, 2048, 40), ([31, 17, 40, 2], 257, 1024, None),
+    ([260, 150, 390], 384, 1280, 333), ([1000, 24], 640, 900, None), ([513], 300, 7168, None),
+    ([2100, 5], 2300, 256, None), ([520, 300], 16640, 512, None),
+    ([64] * 5, 2304, 128, None), ([16], 4096, 8192, None)])
+def test_whole_numbers(counts, N, K, tokens):
+    whole_numbers(counts, N, K, tokens)
+
+
+@pytest.mark.parametrize("counts,N", [
+    ([4] * 8, 2048), ([100], 2048), ([70, 0, 30, 60, 64, 64, 90, 64], 2048), ([300] * 3, 900),
+    ([513], 1500)])
+@pytest.mark.parametrize("K", [128, 500, 640, 2304])
+def test_every_kernel(counts, N, K):
+    """The streaming products by four and eight waves, small tiles of two stages and of
+    four, large tiles, with one stage, an odd number and an even one."""
+    whole_numbers(counts, N, K, 37)
 
 
 def test_scales_of_the_whole_range():
@@ -349,3 +363,78 @@ def test_gradient_against_differences():
     # x + d in -16..16 is held exactly by E4M3
     left = (dy[:, :N].double() * (y(x + d) - y(x))).sum()
     assert left.item() == (dx * d.double()).sum().item()
+
+
+def test_rows_of_x_past_4_GiB():
+    """Gathered rows that no 32-bit offset reaches, in the tile kernel and the streaming one."""
+    gen = torch.Generator().manual_seed(6)
+    K, N, far = 4096, 640, (1 << 20) + 5000
+    one = dict(dtype=torch.uint8, device=DEV)
+    x = torch.zeros(far, K, **one)
+    some = torch.randint(0, far, (900,), generator=gen)
+    some[:4] = torch.tensor([far - 1, 0, 1 << 20, (1 << 20) - 1])
+    values = whole((900, K), gen)
+    x[some.to(DEV)] = values.to(DEV).to(torch.float8_e4m3fn).view(torch.uint8)
+    values = x[some.to(DEV)].view(torch.float8_e4m3fn).float().cpu()  # of rows drawn twice
+    w = whole((2, N, K), gen)
+    wc, ws = w.to(DEV).to(torch.float8_e4m3fn), torch.full((2, 5, 32), 127, **one)
+    xs = torch.full((far, 32), 127, **one)
+    for counts in ([500, 400], [3, 1]):
+        rows = sum(counts)
+        index = some[:rows].to(torch.int32).to(DEV)
+        c = torch.tensor(counts, dtype=torch.int32, device=DEV)
+        y = moe.gmm_fp8(x.view(torch.float8_e4m3fn), xs, wc, ws, c, index=index,
+                        dtype=torch.float32, check=True)
+        assert torch.equal(y.cpu().double(), plain.gmm(values[:rows], w, c)[0])
+
+
+def test_a_gradient_of_rows_past_16_MiB():
+    """Rows of dy longer than a tile's 32-bit offsets allow: 17 million values."""
+    N, K, rows = 17_000_000, 10, 3
+    one = dict(dtype=torch.uint8, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    C = -(-N // 128) * 128
+    dy = torch.zeros(rows, C, device=DEV)
+    dy[:, :N] = torch.randint(-1, 2, (rows, N), generator=gen, device=DEV).float()
+    w = torch.zeros(1, N, 128, device=DEV, dtype=torch.bfloat16)
+    w[:, :, :K] = torch.randint(-1, 2, (1, N, K), generator=gen, device=DEV)
+    strips = C // 128
+    ys = torch.full((rows, -(-strips // 4) * 4), 127, **one)
+    ws = torch.full((1, strips, 4), 127, **one)
+    c = torch.tensor([rows], dtype=torch.int32, device=DEV)
+    dx = moe.gmm_fp8_dx(dy.to(torch.float8_e4m3fn), ys, w.to(torch.float8_e4m3fn), ws, c, cols=K,
+                        dtype=torch.float32, check=True)
+    want = torch.zeros(rows, K, dtype=torch.float64, device=DEV)
+    for at in range(0, N, 1 << 20):
+        part = slice(at, min(N, at + (1 << 20)))
+        want += dy[:, part].double() @ w[0, part, :K].double()
+    assert torch.equal(dx.double(), want)
+
+
+@pytest.mark.parametrize("counts", [[2], [700, 5]])
+def test_an_empty_x(counts):
+    """x without rows: every index lies outside it, every row is a row of zeros."""
+    (_, _), (wc, ws), c, _, _ = operands(counts, 130, 256)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    index = torch.zeros(sum(counts), dtype=torch.int32, device=DEV)
+    y = moe.gmm_fp8(torch.empty(0, 256, dtype=moe.E4M3, device=DEV),
+                    torch.empty(0, 4, dtype=torch.uint8, device=DEV), wc, ws, c, index=index,
+                    status=status)
+    assert status.item() == a2av.ERR_INVALID_ARGS and bool((y == 0).all())
+
+
+def test_two_streams_at_once():
+    """Calls share nothing: two streams' products and conversions side by side."""
+    sets = [operands([300, 40], 256, 640, seed=s) for s in (1, 2)]
+    want = [(moe.gmm_fp8(*s[0], *s[1], s[2]), moe.gmm_fp8_dx(*s[4], *s[1], s[2])) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(8):
+        for i, (s, stream) in enumerate(zip(sets, streams)):
+            got[i].append((moe.gmm_fp8(*s[0], *s[1], s[2], stream=stream),
+                           moe.gmm_fp8_dx(*s[4], *s[1], s[2], stream=stream)))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for pair in g:
+            assert torch.equal(pair[0], w[0]) and torch.equal(pair[1], w[1])

@@ -256,3 +256,32 @@ def test_graph_streams_and_given_outputs(T):
         assert all(torch.equal(a, b) for a, b in zip(out, want))
         assert torch.equal(grad, moe.route_grouped_backward(l, want.experts, want.weights, dw,
                                                             scale=2.5))
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,top", [(300, 4, 2), (512, 8, 3), (256, 64, 9), (1000, 10, 4), (128, 32, 7),
+                                          (60, 20, 5)])
+def test_more_experts_or_groups_than_a_row_of_lanes_has(kind, E, groups, top):
+    """The form with a wave to each token: numbers, near sums, masks, many tokens."""
+    gen = torch.Generator().manual_seed(E)
+    l = torch.randn(700, E, generator=gen) * 2
+    l[3, 4], l[4, 7], l[5, [3, 9]] = NAN, INF, NAN
+    l[6] = -INF
+    l[7, : E // 2] = -INF
+    l[8] = torch.finfo(torch.float32).min
+    bias = torch.randn(E, generator=gen) * (0.1 if kind == "sigmoid" else 0.3 / E)
+    for b in (bias, None):
+        for best in (1, 2):
+            check(l, 5, kind, b, groups, top, best)
+    s = groups_of.scores(l[20].double().numpy(), kind)
+    check(l[20:21].repeat(9, 1), 5, kind, torch.from_numpy(0.75 - s).float(), groups, top)
+    bias[5], bias[6] = NAN, -INF
+    check(l[:40], 5, kind, bias, groups, top)
+
+
+@pytest.mark.parametrize("T", [30, 2000])
+def test_all_alike(T):
+    """Every logit and bias the same: the lowest numbers, in order."""
+    for E, groups, top in ((64, 8, 2), (256, 8, 4), (160, 8, 3), (512, 8, 4)):
+        r = check(torch.zeros(T, E), 6, "sigmoid", torch.zeros(E), groups, top)
+        assert bool((r.experts.cpu() == torch.arange(6)).all())
