@@ -1,7 +1,8 @@
 // moe_fp8.hip -- the products grouped by expert on 8-bit rows and weights.
 //
 // With r a row of expert e, b a block of 128 of the reduction and 2^s the scales
-//   forward  y [r][n] = sum_b 2^(sx[index[r]][b] + sw[e][n / 128][b]) sum_k x[index[r]][k] W[e][n][k]
+//   forward  y [r][n] = sum_b 2^(sx[i][b] + sw[e][n / 128][b]) sum_k x[i][k] W[e][n][k],
+//            i = index[r]
 //   dx       dx[r][k] = sum_b 2^(sdy[r][b] + sw[e][b][k / 128]) sum_n dy[r][n] W[e][n][k]
 // A block is 128 bytes of a row and one matrix instruction, 16 x 16 x 128, which
 // takes both scales as powers of two at no cost.  (FP32 scales would cost four
@@ -9,6 +10,10 @@
 // registers.)  It adds eight neighbouring products after cutting them at 2^-13 of
 // the largest's binade, the eights and the blocks in FP32.  The format fills every
 // row up to whole blocks, so there are no other alignments.
+//   fp8_large, fp8_small  256 x 256 and 128 x 128 tiles of the output, a block per
+//       stage, brought straight to LDS
+//   fp8_few     few rows per expert, forward: W streams into registers
+//   fp8_kernel  128 x 128 tiles with 64-bit addresses, for operands past 4 GiB
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -235,7 +240,7 @@ __device__ inline void load_byte_to_lds(const uint8_t* base, uint32_t offset, ui
 // columns 4 g .. 4 g + 3 of a fragment; of two fragments side by side, groups 2 h and
 // 2 h + 1 exchange halves, so that the even one has 8 columns of the first and the odd
 // one of the second: a store of 16 bytes per lane, 64 in a row.  No LDS, and so no
-// barrier: a 256 x 256 tile by way of LDS took the workgroup some 4 us more.
+// barrier (8192^3 by way of LDS: 431 us for 415).
 template <int TM, int TN, int FM, int FN, class At>
 __device__ inline void store_halves(const GmmParams& p, const Tile& t, const float4v (&acc)[FM][FN],
                                     int wm, int wn, At ready) {
@@ -259,8 +264,10 @@ __device__ inline void store_halves(const GmmParams& p, const Tile& t, const flo
 #pragma unroll
     for (int d = 0; d < FN; d += 2) {
       const float4v u = acc[a][d], v = acc[a][d + 1];
-      const auto x = __builtin_amdgcn_permlane16_swap(two(u[0], u[1]), two(v[0], v[1]), false, false);
-      const auto y = __builtin_amdgcn_permlane16_swap(two(u[2], u[3]), two(v[2], v[3]), false, false);
+      const auto x =
+          __builtin_amdgcn_permlane16_swap(two(u[0], u[1]), two(v[0], v[1]), false, false);
+      const auto y =
+          __builtin_amdgcn_permlane16_swap(two(u[2], u[3]), two(v[2], v[3]), false, false);
       const int4v piece = {int(x[0]), int(y[0]), int(x[1]), int(y[1])};
       const int col = col0 + d * 16;
       if (r >= t.rm || col >= t.cn) continue;
@@ -295,6 +302,12 @@ struct Pipe8 {
 // reads the stage's buffer again and the loads of stage s + NB go there; before it
 // everybody waits for his loads of stage s + 1.
 // The rows that a tile reads lie within 4 GiB of its first.
+// 8192^3: 390 to 415 us, 2,650 to 2,820 TFLOP/s (the library's product with one scale:
+// 2,675), the matrix units busy for 65 % of the cycles at 1.9 to 2.1 GHz.  16384 rows of
+// 16 experts, 2048 x 7168: 245 and, dx, 275 us, of which some 12 us per round of tiles
+// are their starts and ends.  Loads spread over half of a stage's products, evenly: over
+// a quarter of them 5 % slower.  One workgroup per CU that takes a tile after the other,
+// the next one's first loads under the stores of this one, was 2 to 8 % slower.
 template <int MODE, int BM, int BN, int NB>
 __device__ inline void fp8_tile(const GmmParams& p, const Tile& t, uint8_t* lds) {
   using Shape = Pipe8<BM, BN, NB>;
@@ -572,8 +585,8 @@ __global__ __launch_bounds__(256, NB == 2 ? 2 : 1) void fp8_small(const GmmParam
 // rows a weight's bytes are the time: every wave streams its part of W straight into
 // registers, U blocks of its rows at a time, and the waves' sums meet in LDS, in the
 // order of the waves.  A group of four blocks has its scales in one word of a row and
-// one of the weight's.  32 rows of 8 experts, 2048 x 7168: 26 us, 4.6 TB/s of W.
-// Non-temporal loads, which give up the second half of a line, took 30.
+// one of the weight's.  32 rows of 8 experts, 2048 x 7168: 22 us, 5.3 TB/s of W.
+// Non-temporal loads, which give up the second half of a line, took 4 us more.
 template <int MT, int FN, int NW>
 __global__ __launch_bounds__(NW * 64, 4) void fp8_few(const GmmParams p) {
   constexpr int BM = MT * 16, BN = FN * 16, U = 4;
@@ -615,8 +628,8 @@ __global__ __launch_bounds__(NW * 64, 4) void fp8_few(const GmmParams p) {
     const int c = f * 16 + l16;
     w[f] = p.other + (w0 + (c < t.cn ? c : t.cn - 1)) * p.other_stride + g * 16;
   }
-  const uint8_t* ws = uniform(p.other_scales + (int64_t(t.span.e) * ((p.N + 127) / 128) + t.c0 / 128) *
-                                                   scale_bytes(p.blocks));
+  const int64_t strip = int64_t(t.span.e) * ((p.N + 127) / 128) + t.c0 / 128;
+  const uint8_t* ws = uniform(p.other_scales + strip * scale_bytes(p.blocks));
   float4v acc[MT][FN];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
