@@ -307,7 +307,7 @@ struct Pipe8 {
 // 16 experts, 2048 x 7168: 245 and, dx, 275 us, of which some 12 us per round of tiles
 // are their starts and ends.  Loads spread over half of a stage's products, evenly: over
 // a quarter of them 5 % slower.  One workgroup per CU that takes a tile after the other,
-// the next one's first loads under the stores of this one, was 2 to 8 % slower.
+// the next one's first loads under the stores of this one, was 2 to 10 % slower.
 template <int MODE, int BM, int BN, int NB>
 __device__ inline void fp8_tile(const GmmParams& p, const Tile& t, uint8_t* lds) {
   using Shape = Pipe8<BM, BN, NB>;
@@ -585,7 +585,7 @@ __global__ __launch_bounds__(256, NB == 2 ? 2 : 1) void fp8_small(const GmmParam
 // rows a weight's bytes are the time: every wave streams its part of W straight into
 // registers, U blocks of its rows at a time, and the waves' sums meet in LDS, in the
 // order of the waves.  A group of four blocks has its scales in one word of a row and
-// one of the weight's.  32 rows of 8 experts, 2048 x 7168: 22 us, 5.3 TB/s of W.
+// one of the weight's.  32 rows of 8 experts, 2048 x 7168: 22 us in a trace, 5.3 TB/s of W.
 // Non-temporal loads, which give up the second half of a line, took 4 us more.
 template <int MT, int FN, int NW>
 __global__ __launch_bounds__(NW * 64, 4) void fp8_few(const GmmParams p) {
