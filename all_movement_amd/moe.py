@@ -20,9 +20,9 @@ check on device data that failed (it is never cleared); with ``check=True`` the
 call waits and raises instead.
 
 Gradients are calls of their own (``route_backward``, ``route_grouped_backward``,
-``gmm_dx``, ``gmm_dw``, ``gmm_fp8_dx``, ``combine_backward``), for a training step or an autograd function to make; no
-call records one, so that operands that require a gradient are refused unless
-recording is off (``torch.no_grad()``).
+``gmm_dx``, ``gmm_dw``, ``gmm_fp8_dx``, ``combine_backward``), for a training step or
+an autograd function to make; no call records one, so that operands that require a
+gradient are refused unless recording is off (``torch.no_grad()``).
 """
 from __future__ import annotations
 
