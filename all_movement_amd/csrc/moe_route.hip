@@ -290,51 +290,56 @@ __device__ inline uint64_t lane64(uint64_t v, int lane) {
   return uint64_t(uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v)), lane))) |
          uint64_t(uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v >> 32)), lane))) << 32;
 }
-__device__ inline uint64_t wave_max64(uint64_t v) {
-  const uint32_t hi = wave_max(uint32_t(v >> 32));
-  const uint32_t lo = wave_max(uint32_t(v >> 32) == hi ? uint32_t(v) : 0u);
-  return uint64_t(hi) << 32 | lo;
-}
 __device__ inline double wave_sum64(double v) {
   for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
   return v;
 }
 
-// One token by one wave, as the definition says it: scores in 64 bits.  They stand in
-// LDS, so that few registers are taken from the path that nearly every token goes.
-__device__ inline void choose_grouped(const RouteParams& p, int t, int32_t* ids, float* scratch) {
-  const int lane = threadIdx.x & 63, size = p.E / p.groups;
-  uint64_t* const keys = reinterpret_cast<uint64_t*>(scratch);  // 0: not to be chosen
-  auto in_order = [] {  // a wave's LDS accesses are done in order: keep theirs
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  };
-  auto logit = [&](int e) { return load_value(p.logits, int64_t(t) * p.stride + e, p.dtype); };
+// One token by one wave, as the definition says it: scores in 64 bits.  A lane has NE
+// neighbouring experts, so that the first of equal ones is the first lane's first.
+template <int NE>
+__device__ inline void choose_grouped(const RouteParams& p, int t, const float* bias, int32_t* ids,
+                                      float* scratch) {
+  const int lane = threadIdx.x & 63, size = p.E / p.groups, e0 = lane * NE;
+  const float none = -__builtin_inff();
+  Row<NE> l;
+  l.load(p.logits, int64_t(t) * p.stride, p.E, p.dtype,
+         row_pieces<NE>(p.logits, p.stride, p.E, p.dtype));
   double most = 0.0, sum_of_exp = 1.0;
   if (!p.sigmoid) {
-    float top = -__builtin_inff();
-    for (int e = lane; e < p.E; e += 64) top = fmaxf(top, logit(e));
+    float top = none;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) top = fmaxf(top, l.v[i]);
     most = double(wave_fmax(top));
-    sum_of_exp = 0.0;
-    for (int e = lane; e < p.E; e += 64) {
-      const float l = logit(e);
-      sum_of_exp += l == -__builtin_inff() ? 0.0 : exp(double(l) - most);
-    }
+  }
+  auto power = [&](float v) { return exp(p.sigmoid ? -double(v) : double(v) - most); };
+  double x[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) x[i] = l.v[i] == none ? 0.0 : power(l.v[i]);
+  if (!p.sigmoid) {
+    sum_of_exp = x[0];
+#pragma unroll
+    for (int i = 1; i < NE; ++i) sum_of_exp += x[i];
     sum_of_exp = wave_sum64(sum_of_exp);
   }
-  auto score = [&](float l) {
-    const double x = exp(p.sigmoid ? -double(l) : double(l) - most);
-    return p.sigmoid ? 1.0 / (1.0 + x) : x / sum_of_exp;
-  };
-  in_order();
-  for (int e = lane; e < p.E; e += 64) {
-    const float l = logit(e);
-    const double c = p.bias ? score(l) + double(p.bias[e]) : score(l);
-    keys[e] = l == -__builtin_inff() || c == -__builtin_inf() ? 0 : key64_of(c);
+  auto score = [&](double y) { return p.sigmoid ? 1.0 / (1.0 + y) : y / sum_of_exp; };
+  uint64_t key[NE];  // 0: not to be chosen
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const double c = p.bias ? score(x[i]) + double(bias[e0 + i]) : score(x[i]);
+    key[i] = l.v[i] == none || c == -__builtin_inf() ? 0 : key64_of(c);
   }
-  in_order();
   uint64_t allowed = ~0ull;
   if (p.groups > 1) {
+    uint64_t* const keys = reinterpret_cast<uint64_t*>(scratch);
+    auto in_order = [] {  // a wave's LDS accesses are done in order: keep theirs
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    };
+    in_order();
+#pragma unroll
+    for (int i = 0; i < NE; ++i) keys[e0 + i] = key[i];
+    in_order();
     int span = 64;  // lanes of a group
     while (span * p.groups > 64) span >>= 1;
     const int g = lane / span;
@@ -367,30 +372,47 @@ __device__ inline void choose_grouped(const RouteParams& p, int t, int32_t* ids,
     allowed = 0;
     for (int i = 0; i < p.groups; ++i) allowed |= (lanes >> (i * span) & 1) << i;
   }
-  // In whose order experts are taken, 0 for those of other groups.
-  for (int e = lane; e < p.E; e += 64) {
-    const bool ok = keys[e] && allowed >> (p.groups > 1 ? e / size : 0) & 1;
-    if (!ok) keys[e] = 0;
-    else if (!p.bias) keys[e] = key_of(logit(e));
+  // In whose order experts are taken, 0 for those of other groups.  No other key has
+  // zeros for its upper half.
+  int group = p.groups > 1 ? e0 / size : 0, in_group = e0 - group * size;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    if (!(allowed >> (group & 63) & 1)) key[i] = 0;
+    else if (key[i] && !p.bias) key[i] = uint64_t(key_of(l.v[i])) << 32;
+    if (++in_group == size) in_group = 0, ++group;
   }
-  in_order();
   int mine = -1;
   for (int j = 0; j < p.k; ++j) {
-    uint64_t top = 0;
+    uint64_t top = key[0];
     int at = 0;
-    for (int e = lane; e < p.E; e += 64) {
-      const uint64_t k = keys[e];
-      if (k > top) top = k, at = e;
+#pragma unroll
+    for (int i = 1; i < NE; ++i)
+      if (key[i] > top) top = key[i], at = i;
+    const uint32_t hi = wave_max(uint32_t(top >> 32));
+    if (!hi) break;
+    bool is = uint32_t(top >> 32) == hi;
+    uint64_t who = __ballot(is);
+    if (who & (who - 1)) {
+      const uint32_t lo = wave_max(is ? uint32_t(top) : 0u);
+      is = is && uint32_t(top) == lo;
+      who = __ballot(is);
     }
-    const uint64_t first = wave_max64(top);
-    if (!first) break;
-    const int e = int(~wave_max(top == first ? ~uint32_t(at) : 0u));  // the lowest of them
+    const int from = __ffsll((unsigned long long)who) - 1;
+    const int e = from * NE + __builtin_amdgcn_readlane(at, from);
     if (lane == j) mine = e;
-    if (top == first && at == e) keys[e] = 0;
+    if (lane == from) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (i == at) key[i] = 0;
+    }
   }
-  const double s = mine >= 0 ? score(logit(mine)) : 0.0;
+  double s = 0.0;
+  if (mine >= 0) s = score(power(load_value(p.logits, int64_t(t) * p.stride + mine, p.dtype)));
   double total = 1.0;
-  if (p.renorm) total = wave_sum64(s);
+  if (p.renorm) {  // over the lanes that have slots
+    total = s;
+    for (int d = 1; d < 16; d <<= 1) total += __shfl_xor(total, d);
+  }
   if (lane < p.k) {
     const int64_t slot = int64_t(t) * p.k + lane;
     p.experts[slot] = mine;
@@ -865,7 +887,7 @@ __device__ inline void choose_all(const RouteParams& p, int t0, int n, const flo
       const uint64_t left = __ballot(!done);
       for (int r = 0; r < 4; ++r)
         if (first + r < n && left >> (r * 16) & 1)
-          choose_grouped(p, t0 + first + r, ids + (first + r) * p.k, scratch);
+          choose_grouped<PER / 4>(p, t0 + first + r, bias, ids + (first + r) * p.k, scratch);
     }
   } else {
     Groups<GROUPED ? PER : 1, 64> groups;
@@ -879,7 +901,7 @@ __device__ inline void choose_all(const RouteParams& p, int t0, int n, const flo
         next.load(p.logits, int64_t(t0 + t + kWaves) * p.stride, p.E, p.dtype, vec);
       if constexpr (GROUPED) {
         if (!choose_near<PER>(p, t0 + t, row.v, groups, bias, ids + t * p.k, scratch))
-          choose_grouped(p, t0 + t, ids + t * p.k, scratch);
+          choose_grouped<PER>(p, t0 + t, bias, ids + t * p.k, scratch);
       } else {
         choose<PER>(p, t0 + t, row.v, ids + t * p.k);
       }
