@@ -302,6 +302,10 @@ __device__ inline void choose_grouped(const RouteParams& p, int t, const float* 
                                       float* scratch) {
   const int lane = threadIdx.x & 63, size = p.E / p.groups, e0 = lane * NE;
   const float none = -__builtin_inff();
+  auto in_order = [] {  // a wave's LDS accesses are done in order: keep theirs
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
   Row<NE> l;
   l.load(p.logits, int64_t(t) * p.stride, p.E, p.dtype,
          row_pieces<NE>(p.logits, p.stride, p.E, p.dtype));
@@ -312,10 +316,12 @@ __device__ inline void choose_grouped(const RouteParams& p, int t, const float* 
     for (int i = 0; i < NE; ++i) top = fmaxf(top, l.v[i]);
     most = double(wave_fmax(top));
   }
-  auto power = [&](float v) { return exp(p.sigmoid ? -double(v) : double(v) - most); };
   double x[NE];
 #pragma unroll
-  for (int i = 0; i < NE; ++i) x[i] = l.v[i] == none ? 0.0 : power(l.v[i]);
+  for (int i = 0; i < NE; ++i) {
+    const double v = double(l.v[i]);
+    x[i] = l.v[i] == none ? 0.0 : exp(p.sigmoid ? -v : v - most);
+  }
   if (!p.sigmoid) {
     sum_of_exp = x[0];
 #pragma unroll
@@ -332,10 +338,6 @@ __device__ inline void choose_grouped(const RouteParams& p, int t, const float* 
   uint64_t allowed = ~0ull;
   if (p.groups > 1) {
     uint64_t* const keys = reinterpret_cast<uint64_t*>(scratch);
-    auto in_order = [] {  // a wave's LDS accesses are done in order: keep theirs
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    };
     in_order();
 #pragma unroll
     for (int i = 0; i < NE; ++i) keys[e0 + i] = key[i];
@@ -381,6 +383,11 @@ __device__ inline void choose_grouped(const RouteParams& p, int t, const float* 
     else if (key[i] && !p.bias) key[i] = uint64_t(key_of(l.v[i])) << 32;
     if (++in_group == size) in_group = 0, ++group;
   }
+  double* const powers = reinterpret_cast<double*>(scratch);
+  in_order();
+#pragma unroll
+  for (int i = 0; i < NE; ++i) powers[e0 + i] = x[i];
+  in_order();
   int mine = -1;
   for (int j = 0; j < p.k; ++j) {
     uint64_t top = key[0];
@@ -406,8 +413,7 @@ __device__ inline void choose_grouped(const RouteParams& p, int t, const float* 
         if (i == at) key[i] = 0;
     }
   }
-  double s = 0.0;
-  if (mine >= 0) s = score(power(load_value(p.logits, int64_t(t) * p.stride + mine, p.dtype)));
+  const double s = mine >= 0 ? score(powers[mine]) : 0.0;
   double total = 1.0;
   if (p.renorm) {  // over the lanes that have slots
     total = s;
