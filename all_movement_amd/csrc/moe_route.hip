@@ -1268,6 +1268,18 @@ static hipError_t launch_route_of(const RouteParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The router by groups with a wave to each token is the shorter way as long as no wave
+// has two of them (to 2303 tokens where they are too many for one workgroup).  us of
+// four tokens to a wave and of one, 256 experts in 8 groups: 1 token 9.3 and 7.0, 8
+// tokens 9.6 and 7.7, 12 tokens 9.6 and 10.0, 48 tokens 14.5 and 24.0; in three launches
+// 64 tokens 16.2 and 12.5, 1024 tokens 17.1 and 13.3, 2048 tokens 19.8 and 18.3, 4096
+// tokens 22.6 and 22.4, 8192 tokens 23.8 and 29.1; 64 experts in one group, 8 tokens 6.1
+// and 5.3, 2048 tokens 11.7 and 11.3, 4096 tokens 13.6 and 14.5.
+static bool a_token_each(const RouteParams& p) {
+  return p.tokens <= kWaves ||
+         (!route_is_small(p.tokens, p.E, p.k) && route_per_block(p.tokens) <= kWaves);
+}
+
 hipError_t launch_route(RouteParams p, hipStream_t stream) {
   (void)hipGetLastError();
   p.per_block = route_per_block(p.tokens);
@@ -1276,7 +1288,7 @@ hipError_t launch_route(RouteParams p, hipStream_t stream) {
     with_per(p.E, [&](auto per) {
       e = launch_route_of<decltype(per)::value, false, false>(p, stream);
     });
-  } else if (p.E <= 256 && p.groups <= 16) {
+  } else if (p.E <= 256 && p.groups <= 16 && !a_token_each(p)) {
     // Four tokens to a wave: every wave of a block has some.
     if (p.per_block < kWaves * 4) p.per_block = kWaves * 4;
     if (p.E <= 64) e = launch_route_of<4, true, true>(p, stream);

@@ -42,7 +42,8 @@ def check(logits, k, kind="sigmoid", bias=None, groups=1, top=None, best=2, reno
 SIZES = [(1, 1, 1, 1, 1), (3, 8, 2, 2, 1), (16, 256, 8, 8, 4), (37, 100, 5, 5, 2), (300, 256, 8, 8, 4),
          (129, 160, 6, 8, 3), (1000, 18, 3, 6, 3), (100, 1000, 16, 10, 4), (64, 512, 16, 64, 7),
          (65, 64, 16, 64, 20), (300, 1024, 8, 32, 8), (700, 6, 2, 1, 1), (1025, 3, 1, 3, 2),
-         (49, 96, 4, 3, 1), (257, 44, 7, 4, 4)]
+         (49, 96, 4, 3, 1), (257, 44, 7, 4, 4), (9, 256, 8, 8, 4), (33, 120, 6, 10, 4),
+         (2400, 256, 8, 8, 4), (2500, 96, 4, 3, 1), (3001, 60, 5, 12, 5)]
 
 
 @pytest.mark.parametrize("dt", DTYPES)
@@ -58,7 +59,7 @@ def test_against_definition(dt, kind, best, renorm, biased, scale, T, E, k, grou
 
 
 @pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
-@pytest.mark.parametrize("T", [5, 900])
+@pytest.mark.parametrize("T", [5, 20, 900, 2400])
 @pytest.mark.parametrize("biased", [True, False])
 def test_ties_and_masks(T, kind, biased):
     gen = torch.Generator().manual_seed(9)
@@ -85,7 +86,7 @@ def test_ties_and_masks(T, kind, biased):
 
 
 def test_every_token_without_experts():
-    for T in (20, 300):
+    for T in (6, 20, 300, 2400):
         r = check(torch.full((T, 40), -INF), 8, "softmax", None, 4, 2)
         assert r.counts.sum().item() == 0 and bool((r.order == -1).all())
         r = check(torch.full((T, 40), -INF), 8, "sigmoid", torch.zeros(40), 4, 2)
@@ -94,7 +95,8 @@ def test_every_token_without_experts():
 
 @pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("biased", [True, False])
-def test_logits_that_are_no_numbers(kind, biased):
+@pytest.mark.parametrize("times", [1, 3, 100, 350])
+def test_logits_that_are_no_numbers(kind, biased, times):
     l = torch.randn(7, 20, generator=torch.Generator().manual_seed(1))
     l[0, 4] = NAN
     l[1, 7] = INF
@@ -102,6 +104,7 @@ def test_logits_that_are_no_numbers(kind, biased):
     l[3, [2, 5]] = INF
     l[4, 3], l[4, 16] = NAN, -INF
     l[5, :5], l[5, 11] = -INF, NAN
+    l = l.repeat(times, 1)
     bias = torch.randn(20, generator=torch.Generator().manual_seed(2)) * 0.1 if biased else None
     for groups, top in ((1, 1), (4, 2), (5, 1)):
         for renorm in (True, False):
@@ -111,7 +114,7 @@ def test_logits_that_are_no_numbers(kind, biased):
         check(l, 3, kind, bias, 4, 2)
 
 
-@pytest.mark.parametrize("T", [7, 200])
+@pytest.mark.parametrize("T", [7, 21, 200, 2400])
 @pytest.mark.parametrize("E,groups,top", [(64, 1, 1), (64, 8, 3), (256, 8, 4), (100, 5, 2)])
 def test_sums_that_only_64_bits_tell_apart(T, E, groups, top):
     """Biases that bring every score to the same number, up to their own rounding."""
@@ -279,7 +282,7 @@ def test_more_experts_or_groups_than_a_row_of_lanes_has(kind, E, groups, top):
     check(l[:40], 5, kind, bias, groups, top)
 
 
-@pytest.mark.parametrize("T", [30, 2000])
+@pytest.mark.parametrize("T", [8, 30, 2000, 2310])
 def test_all_alike(T):
     """Every logit and bias the same: the lowest numbers, in order."""
     for E, groups, top in ((64, 8, 2), (256, 8, 4), (160, 8, 3), (512, 8, 4)):
