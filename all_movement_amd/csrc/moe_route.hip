@@ -492,8 +492,8 @@ struct Groups {
 __device__ inline float apart(const RouteParams& p) { return p.sigmoid ? 0x1p-20f : 0x1p-18f; }
 
 // choose_grouped in FP32, as far as that can tell the experts and groups apart; false,
-// and nothing written, when it cannot (32768 tokens of 256 experts with their
-// gradient: 186 us with every token by 64 bits, 80 with those alone that need them).
+// and nothing written, when it cannot (256 tokens of 256 experts: 13 us, 16 with
+// every one by 64 bits; 4096 tokens 22 and 41).
 template <int PER>
 __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)[PER],
                                    const Groups<PER, 64>& groups, const float* bias,
