@@ -483,13 +483,25 @@ struct Groups {
 
 // How far apart sums of score and bias have to be, in FP32, to stand in their true
 // order, as a part of `reach`, the token's largest score (sigmoid: 1), and of the sum
-// itself; groups' scores, of two, twice as far.  One step is 2^-23 of a value.  exp is
-// within 1.5 steps.  Sigmoid: past 1/2 half of that, 1 + x within half a step and its
-// inverse within one, 2^-22; below 1/2 a product's half step more, 2^-21.3 of less than
-// 1/2; with the sum's rounding two are off by less than 2 (2^-22 + 2^-24).  Softmax: the
-// argument's rounding (x e^x < 0.37) and the product with the inverse, 2^-21.9 each, and
-// what all have in common, the sum of 16 and 6 terms, 22 half steps of their distance.
+// itself.  One step is 2^-23 of a value; exp is within 2 steps, the inverse within one.
+// Sigmoid: past 1/2 a quarter of exp's error, half a step of 1 + x and one of the
+// inverse, 2^-22; below 1/2 half of exp's and a product's half step more, of less than
+// 1/2, which is less.  Two are off by 2^-21, and by 2^-23 of the sums for adding the bias.
+// Softmax: exp's 2 steps, its argument's rounding (y e^y < 0.37) and the product with the
+// inverse, 2^-21.6 each.  What all have in common, the sum's error, moves two by its part
+// of their distance: 2 steps of exp, 5 half steps of arguments (the mean of |y| over 1024
+// terms), 22 of 16 and 6 additions, 5 of the inverse, 2^-18.8.  Together 2^-18.4.
 __device__ inline float apart(const RouteParams& p) { return p.sigmoid ? 0x1p-20f : 0x1p-18f; }
+
+// How far a group's score, the FP32 sum of its best sums `one` and `two` (-inf if it has
+// no other), may be off: every one of them has its own error, which their sum, if they
+// are of opposite signs, may be smaller than.  The bound rises with a sum's magnitude
+// less than the sum, so it holds for whichever are the best in 64 bits.
+__device__ inline float group_off(const RouteParams& p, float reach, float one, float two) {
+  float size = fabsf(one);
+  if (p.group_best == 2 && two != -__builtin_inff()) size += fabsf(two);
+  return apart(p) * (reach + size);
+}
 
 // choose_grouped in FP32, as far as that can tell the experts and groups apart; false,
 // and nothing written, when it cannot (256 tokens of 256 experts: 13 us, 16 with
@@ -573,15 +585,11 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
       rank += s > score || (s == score && g < group);
     }
     const bool is = mine && score != none;
-    // The last group that is taken and the first that is not.
-    const uint64_t last = __ballot(is && rank == p.top_groups - 1);
-    const uint64_t next = __ballot(is && rank == p.top_groups);
-    if (last && next && !by_logit) {
-      const float a = __int_as_float(__builtin_amdgcn_readlane(
-          __float_as_int(score), __ffsll((unsigned long long)last) - 1));
-      const float b = __int_as_float(__builtin_amdgcn_readlane(
-          __float_as_int(score), __ffsll((unsigned long long)next) - 1));
-      if (!(a - b > 2 * apart(p) * (reach + fabsf(a)))) return false;
+    if (!by_logit) {  // the least that one taken can be, and the most that another can
+      const float off = group_off(p, reach, one, two);
+      const float least = -wave_fmax(is && rank < p.top_groups ? off - score : none);
+      const float other = wave_fmax(is && rank >= p.top_groups ? score + off : none);
+      if (!(least > other)) return false;
     }
     const uint64_t lanes = __ballot(is && rank < p.top_groups);
     if (groups.span) {
@@ -771,12 +779,14 @@ __device__ inline bool choose_rows(const RouteParams& p, int64_t t, bool there,
           0, __float_as_int(score), 0x150 + decltype(n)::value, 0xf, 0xf, true));
       above += s > score || (s == score && decltype(n)::value < group * span);
     });
-    const bool is = score != none;
-    // The last group that is taken and the first that is not.
-    const float a = row_fmax(is && above == (p.top_groups - 1) * span ? score : none);
-    const float b = row_fmax(is && above == p.top_groups * span ? score : none);
-    if (!by_logit && b != none) slow = slow || !(a - b > 2 * apart(p) * (reach + fabsf(a)));
-    allowed = row_ballot(is && above < p.top_groups * span);
+    const bool is = score != none, in = above < p.top_groups * span;
+    if (!by_logit) {  // the least that one taken can be, and the most that another can
+      const float off = group_off(p, reach, one, two);
+      const float least = -row_fmax(is && in ? off - score : none);
+      const float other = row_fmax(is && !in ? score + off : none);
+      slow = slow || !(least > other);
+    }
+    allowed = row_ballot(is && in);
   }
   // A bit for each of the lane's experts whose group is taken.
   uint32_t taken = allowed >> (groups.first * span & 15) & 1 ? 0xffff : 0;
