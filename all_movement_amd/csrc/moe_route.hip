@@ -493,10 +493,17 @@ struct Groups {
 // terms), 22 of 16 and 6 additions, 5 of the inverse, 2^-18.8.  Together 2^-18.4.
 __device__ inline float apart(const RouteParams& p) { return p.sigmoid ? 0x1p-20f : 0x1p-18f; }
 
-// How far a group's score, the FP32 sum of its best sums `one` and `two` (-inf if it has
-// no other), may be off: every one of them has its own error, which their sum, if they
-// are of opposite signs, may be smaller than.  The bound rises with a sum's magnitude
-// less than the sum, so it holds for whichever are the best in 64 bits.
+// A group's score from its best sums `one` and `two` (-inf where it has none).  A sum past
+// the range stays a number, so that the group counts as one with experts; its group_off is
+// infinite.
+__device__ inline float group_score(const RouteParams& p, float one, float two) {
+  if (p.group_best == 1 || two == -__builtin_inff()) return one;
+  return fmaxf(one + two, -0x1.fffffep127f);
+}
+
+// How far that may be off: `one` and `two` have their own errors, which their sum, if they
+// are of opposite signs, may be smaller than.  The bound rises with a sum's magnitude less
+// than the sum, so it holds for whichever are the best in 64 bits.
 __device__ inline float group_off(const RouteParams& p, float reach, float one, float two) {
   float size = fabsf(one);
   if (p.group_best == 2 && two != -__builtin_inff()) size += fabsf(two);
@@ -576,7 +583,7 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
     }
     join_best<1>(one, two, span);
     const bool mine = group < p.groups;
-    float score = p.group_best == 2 && two != none ? one + two : one;
+    float score = group_score(p, one, two);
     if (!mine) score = none;
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
@@ -771,7 +778,7 @@ __device__ inline bool choose_rows(const RouteParams& p, int64_t t, bool there,
           add(scratch[group * groups.size + i]);
     }
     join_best<1>(one, two, span);
-    float score = p.group_best == 2 && two != none ? one + two : one;
+    float score = group_score(p, one, two);
     if (group >= p.groups) score = none;
     int above = 0;  // lanes of groups before this one
     each16([&](auto n) {

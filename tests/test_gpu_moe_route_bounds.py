@@ -92,3 +92,23 @@ def test_four_experts_that_cancel():
     for T in TOKENS:
         r = check(l, T, 2, "sigmoid", torch.tensor([64.0, -64.0, 64.0, -64.0]), 2, 1)
         assert bool((r.experts == torch.tensor([0, 1], device=DEV)).all())
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("E,groups,top", SHAPES)
+def test_biases_of_the_lowest_value(kind, T, E, groups, top):
+    """As a mask on whole groups and on single experts: they come last, but they come."""
+    gen = torch.Generator().manual_seed(E)
+    l = torch.randn(min(T, 25), E, generator=gen)
+    size = E // groups
+    k = min(16, top * size)
+    for low in (LOWEST, -2.0 ** 127):
+        bias = torch.randn(E, generator=gen) * 0.01
+        bias[size:] = low  # all but the first group
+        for best in (1, 2):
+            r = check(l, T, k, kind, bias, groups, top, best)
+            assert bool((r.experts >= 0).all())
+            check(l, T, k, kind, bias, groups, groups, best)
+        bias[1::2] = low
+        check(l, T, k, kind, bias, groups, top)
