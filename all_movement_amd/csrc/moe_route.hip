@@ -510,6 +510,15 @@ __device__ inline float group_off(const RouteParams& p, float reach, float one, 
   return apart(p) * (reach + size);
 }
 
+// Without a bias a group of one best score stands by its best logit `l`, exactly. Whether
+// any other logit's score differs from that of `l` in 64 bits too: the next one lies 2^-24 |l|
+// away or more, and so, 2^-40 at least, does its exponential as a part of itself; a sigmoid's
+// part of that is e^-l, 2^-43 at least.  Past these limits scores of 64 bits meet, as 1, as 0
+// or beside 1/2.
+__device__ inline bool logit_tells(const RouteParams& p, float l, float most) {
+  return fabsf(l) >= 0x1p-16f && (p.sigmoid ? l >= -600.0f && l <= 16.0f : l - most >= -600.0f);
+}
+
 // choose_grouped in FP32, as far as that can tell the experts and groups apart; false,
 // and nothing written, when it cannot (256 tokens of 256 experts: 13 us, 16 with
 // every one by 64 bits; 4096 tokens 22 and 41).
@@ -592,7 +601,14 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
       rank += s > score || (s == score && g < group);
     }
     const bool is = mine && score != none;
-    if (!by_logit) {  // the least that one taken can be, and the most that another can
+    if (by_logit) {
+      const uint64_t last = __ballot(is && rank == p.top_groups - 1);
+      if (last && __ballot(is && rank == p.top_groups)) {
+        const float l = __int_as_float(__builtin_amdgcn_readlane(
+            __float_as_int(score), __ffsll((unsigned long long)last) - 1));
+        if (!logit_tells(p, l, most)) return false;
+      }
+    } else {  // the least that one taken can be, and the most that another can
       const float off = group_off(p, reach, one, two);
       const float least = -wave_fmax(is && rank < p.top_groups ? off - score : none);
       const float other = wave_fmax(is && rank >= p.top_groups ? score + off : none);
@@ -787,7 +803,11 @@ __device__ inline bool choose_rows(const RouteParams& p, int64_t t, bool there,
       above += s > score || (s == score && decltype(n)::value < group * span);
     });
     const bool is = score != none, in = above < p.top_groups * span;
-    if (!by_logit) {  // the least that one taken can be, and the most that another can
+    if (by_logit) {
+      const bool last = is && above == (p.top_groups - 1) * span;
+      const bool more = row_ballot(is && !in) != 0;
+      slow = slow || (more && last && !logit_tells(p, score, most));
+    } else {  // the least that one taken can be, and the most that another can
       const float off = group_off(p, reach, one, two);
       const float least = -row_fmax(is && in ? off - score : none);
       const float other = row_fmax(is && !in ? score + off : none);

@@ -112,3 +112,47 @@ def test_biases_of_the_lowest_value(kind, T, E, groups, top):
             check(l, T, k, kind, bias, groups, groups, best)
         bias[1::2] = low
         check(l, T, k, kind, bias, groups, top)
+
+
+# Logits of each kind that have equal scores in 64 bits: past 37 a sigmoid is 1, below -745
+# it is 0, near 0 it is 1/2; softmax beside 0 has exp(l), 1 or 0.
+LEVELS = {"sigmoid": [38.0, 40.0, 41.0, 55.0, 300.0, 1.0, -800.0, -900.0, LOWEST],
+          "softmax": [0.0, -1e-17, -2e-17, -1.0, -800.0, -801.0, -900.0, LOWEST]}
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("E,groups,top", SHAPES)
+def test_distinct_logits_of_equal_scores(kind, T, E, groups, top):
+    """Groups of equal scores go by their number, without a bias too; experts by logits."""
+    gen = torch.Generator().manual_seed(E)
+    n, size = min(T, 60), E // groups
+    levels = torch.tensor(LEVELS[kind])
+    l = levels[torch.randint(0, len(levels), (n, E), generator=gen)]
+    l[n // 2:] -= 1000  # a best logit of each group that is not the token's largest
+    l[n // 2:].clamp_(min=LOWEST)
+    at = torch.randint(0, len(levels), (n - n // 2, groups), generator=gen)
+    l[n // 2:].view(-1, groups, size)[:, :, -1] = levels[at]
+    if kind == "sigmoid":
+        l[n // 4:n // 2] = torch.tensor([1e-17, 2e-17, -3e-17, 0.0])[
+            torch.randint(0, 4, (n // 2 - n // 4, E), generator=gen)]
+    for best in (1, 2):
+        check(l, T, min(3, top * size), kind, None, groups, top, best, renorm=False)
+
+
+def test_two_saturated_groups():
+    l = torch.tensor([[40.0, 50.0], [40.0, 41.0]])
+    for T in TOKENS:
+        r = check(l, T, 1, "sigmoid", None, 2, 1, 1)
+        assert bool((r.experts == 0).all())
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T", TOKENS)
+def test_groups_by_their_best_logit(dt, T):
+    """Ordinary logits without a bias, many of them alike."""
+    gen = torch.Generator().manual_seed(T)
+    l = (torch.randn(min(T, 150), 96, generator=gen) * 8).round().div(4).to(dt)
+    for kind in ("sigmoid", "softmax"):
+        check(l, T, 5, kind, None, 12, 4, 1)
+        check(l * 8, T, 5, kind, None, 12, 4, 1)
