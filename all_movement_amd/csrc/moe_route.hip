@@ -422,7 +422,7 @@ __device__ inline void choose_grouped(const RouteParams& p, int t, const float* 
   if (lane < p.k) {
     const int64_t slot = int64_t(t) * p.k + lane;
     p.experts[slot] = mine;
-    p.weights[slot] = mine < 0 || total == 0.0 ? 0.0f : float(double(p.scale) * s / total);
+    p.weights[slot] = mine < 0 || total == 0.0 ? 0.0f : float(double(p.scale) * (s / total));
     ids[lane] = mine;
   }
 }
@@ -518,6 +518,10 @@ __device__ inline float group_off(const RouteParams& p, float reach, float one, 
 __device__ inline bool logit_tells(const RouteParams& p, float l, float most) {
   return fabsf(l) >= 0x1p-16f && (p.sigmoid ? l >= -600.0f && l <= 16.0f : l - most >= -600.0f);
 }
+
+// Whether a slot's score s, of exp(y), may lose places to FP32's smallest numbers, which the
+// sum over the slots or the scale can bring back; past -800 it is 0 in 64 bits too.
+__device__ inline bool too_small(float y, float s) { return !(s > 0x1p-100f) && y >= -800.0f; }
 
 // choose_grouped in FP32, as far as that can tell the experts and groups apart; false,
 // and nothing written, when it cannot (256 tokens of 256 experts: 13 us, 16 with
@@ -661,18 +665,21 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
     }
   }
   float s = 0.0f;
+  bool small = false;
   if (mine >= 0) {
-    const float x = exp_of(p.sigmoid ? -fabsf(l) : l - most);
+    const float y = p.sigmoid ? -fabsf(l) : l - most, x = exp_of(y);
     s = !p.sigmoid ? x : (l > 0.0f ? 1.0f : x) / (1.0f + x);
+    small = too_small(y, s);
   }
   if (p.renorm) {
     total = wave_sum(s);
-    if (n && !(total > 0x1p-80f)) return false;
+    small = small || (n && !(total > 0.0f));
   }
+  if (__ballot(small)) return false;
   if (lane < p.k) {
     const int64_t slot = int64_t(t) * p.k + lane;
     p.experts[slot] = mine;
-    p.weights[slot] = mine >= 0 ? p.scale * s / total : 0.0f;
+    p.weights[slot] = mine >= 0 ? p.scale * (s / total) : 0.0f;
     ids[lane] = mine;
   }
   return true;
@@ -888,17 +895,18 @@ __device__ inline bool choose_rows(const RouteParams& p, int64_t t, bool there,
   }
   float s = 0.0f;
   if (q < n) {
-    const float x = exp_of(p.sigmoid ? -fabsf(l) : l - most);
+    const float y = p.sigmoid ? -fabsf(l) : l - most, x = exp_of(y);
     s = !p.sigmoid ? x : (l > 0.0f ? 1.0f : x) / (1.0f + x);
+    slow = slow || too_small(y, s);
   }
   if (p.renorm) {
     total = row_sum(s);
-    slow = slow || (n && !(total > 0x1p-80f));
+    slow = slow || (n && !(total > 0.0f));
   }
   const bool done = row_ballot(slow) == 0;
   if (there && done && q < p.k) {
     p.experts[t * p.k + q] = mine;
-    p.weights[t * p.k + q] = mine >= 0 ? p.scale * s / total : 0.0f;
+    p.weights[t * p.k + q] = mine >= 0 ? p.scale * (s / total) : 0.0f;
     ids[q] = mine;
   }
   return done;

@@ -41,7 +41,8 @@ def check(some, T, k, kind, bias=None, groups=1, top=1, best=2, renorm=True, sca
                           top_groups=top, group_best=best, renormalize=renorm, scale=scale)
     experts, weights, _, _, _ = groups_of.route(
         some.float().numpy(), k, kind, None if bias is None else bias.numpy(), groups, top, best,
-        renorm, scale)
+        renorm, 1.0)
+    weights *= scale  # last: times scores of e^-700 first it would leave float64
     assert np.array_equal(r.experts.cpu().numpy(), experts[at.numpy()])
     want, got = weights[at.numpy()], r.weights.cpu().numpy()
     # Half of the smallest number where a weight is below the normal ones.
@@ -156,3 +157,30 @@ def test_groups_by_their_best_logit(dt, T):
     for kind in ("sigmoid", "softmax"):
         check(l, T, 5, kind, None, 12, 4, 1)
         check(l * 8, T, 5, kind, None, 12, 4, 1)
+
+
+# ---------------------------------------------------------------- weights
+
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("E,groups,top", [(60, 1, 1), (60, 5, 2), (256, 1, 1), (256, 8, 4),
+                                          (300, 1, 1), (300, 5, 2)])
+@pytest.mark.parametrize("scale", [2.0 ** -100, 1.0, 2.0 ** 100])
+def test_weights_of_small_scores(T, E, groups, top, scale):
+    """Scores far below 1, and scales of the whole range: a weight is as near as others."""
+    gen = torch.Generator().manual_seed(E)
+    l = torch.randn(min(T, 60), E, generator=gen)
+    for far in (42.0, 62.0, 69.0, 85.0, 100.0):
+        for renorm in (True, False):
+            check(l - far, T, 6, "sigmoid", None, groups, top, 1, renorm, scale)
+            m = l - far
+            m[:, 0] = 0.0  # softmax: one above all others
+            check(m, T, 6, "softmax", None, groups, top, 1, renorm, scale)
+    m = l - 700.0
+    check(m, T, 6, "sigmoid", None, groups, top, 1, True, scale)
+    m[:, 0] = 0.0
+    bias = torch.zeros(E)
+    bias[0] = -2.0  # its group does without it
+    check(m, T, 6, "softmax", bias, groups, top, 1, True, scale)
+    # Masked by the lowest value: their scores are 0.
+    m[:, 1:] = LOWEST
+    check(m, T, 6, "softmax", None, groups, top, 1, True, scale)
