@@ -184,3 +184,96 @@ def test_weights_of_small_scores(T, E, groups, top, scale):
     # Masked by the lowest value: their scores are 0.
     m[:, 1:] = LOWEST
     check(m, T, 6, "softmax", None, groups, top, 1, True, scale)
+
+
+# ---------------------------------------------------------------- the gradient
+
+def gradient(logits, experts, dweights, kind, renorm, scale):
+    """The gradient in float64, and for each entry the magnitudes that errors go with: its
+    score's slope times the sum of the magnitudes in its bracket."""
+    T, E = logits.shape
+    out, size = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        l = logits[t].astype(np.float64)
+        s = groups_of.scores(l, kind)
+        slots = np.nonzero(experts[t] >= 0)[0]
+        at, g = experts[t][slots], dweights[t][slots].astype(np.float64)
+        total = s[at].sum() if renorm else 1.0
+        u = s[at] / total if total > 0 else np.zeros(len(at))
+        if kind == "softmax" and not renorm:
+            ds = np.zeros(E)
+            ds[at] = g
+            out[t] = s * scale * (ds - u @ g)
+            size[t] = s * scale * (np.abs(ds) + u @ np.abs(g))
+            continue
+        slope = scale * u
+        if kind == "sigmoid":
+            slope = slope * (1 / (1 + np.exp(l[at])))
+        if renorm:
+            out[t, at] = slope * ((g[:, None] - g) @ u)
+            size[t, at] = slope * (np.abs(g[:, None] - g) @ u)
+        else:
+            out[t, at] = slope * g
+            size[t, at] = np.abs(slope * g)
+    return out, size
+
+
+def check_gradient(l, rows, k, kind, bias, groups, top, renorm, scale, gen):
+    """The gradient of rows, l's values on the GPU; what the tolerance is for each entry."""
+    dt, (T, E) = l.dtype, l.shape
+    r = moe.route_grouped(rows, k, scores=kind, bias=bias, groups=groups, top_groups=top,
+                          renormalize=renorm, scale=scale)
+    experts = r.experts.cpu().numpy()
+    dw = torch.randn(T, k, generator=gen)
+    got = moe.route_grouped_backward(rows, r.experts, r.weights, dw.to(DEV), scores=kind,
+                                     renormalize=renorm, scale=scale).double().cpu().numpy()
+    want, size = gradient(l.float().numpy(), experts, dw.numpy(), kind, renorm, scale)
+    oracle = groups_of.route_back(l.float().numpy(), experts, np.where(experts < 0, 0, dw.numpy()),
+                                  kind, renorm, scale)
+    # The oracle's sums of terms up to 2 scale g cancel: (k + 2) 2^-53 of that, 1e-14 at most.
+    most = scale * dw.abs().max().item()
+    assert np.all(np.abs(want - oracle) <= 1e-14 * most + 1e-14 * size)
+    # The slope has a weight's or a score's error and 8 steps more (1 - s: exp within 2, a
+    # sum, a quotient; products); the bracket a weight's, and 2 steps a term.
+    tol = (2 * weight_tol(E) + (2 * k + 12) * 2.0 ** -23) * size
+    if kind == "softmax" and not renorm:  # a score below the normal numbers counts as 0
+        tol += 2.0 ** -126 * 2 * most
+    tol += plain.step(dt) * np.abs(want)
+    tol += torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
+    worst = np.max(np.abs(got - want) - tol)
+    assert worst <= 0, worst
+    return want, size, tol
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k,groups,top,pad", [
+    (3, 5, 2, 1, 1, 0), (70, 64, 4, 8, 2, 0), (70, 100, 5, 5, 2, 0), (40, 256, 8, 8, 4, 0),
+    (40, 130, 8, 2, 1, 1), (30, 300, 8, 4, 2, 0), (30, 512, 8, 8, 4, 0), (30, 512, 8, 8, 4, 3),
+    (20, 1001, 16, 7, 3, 0), (20, 1024, 16, 8, 4, 0)])
+def test_gradient_entry_by_entry(dt, kind, renorm, T, E, k, groups, top, pad):
+    gen = torch.Generator().manual_seed(E)
+    l = (torch.randn(T, E, generator=gen) * 3).to(dt)
+    l[1, E // 2:] = -INF
+    rows = torch.zeros(T, E + pad, dtype=dt, device=DEV)[:, :E]  # pad: rows that are no pieces
+    rows.copy_(l)
+    bias = (torch.randn(E, generator=gen) * 0.05).to(DEV)
+    want, size, tol = check_gradient(l, rows, k, kind, bias, groups, top, renorm, 2.5, gen)
+    # What the tolerance can see: nearly every entry that is not 0.
+    seen = size > 0
+    if dt is not torch.float16:
+        assert np.mean(np.abs(want[seen]) > tol[seen]) > 0.9
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** 100])
+@pytest.mark.parametrize("E", [48, 512])
+def test_gradient_of_small_scores(kind, renorm, scale, E):
+    gen = torch.Generator().manual_seed(E)
+    for far in (40.0, 60.0, 80.0):
+        l = torch.randn(20, E, generator=gen) - far
+        if kind == "softmax":
+            l[:, 1] = 0.0
+        check_gradient(l, l.to(DEV), 6, kind, None, 1, 1, renorm, scale, gen)
