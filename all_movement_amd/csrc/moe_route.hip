@@ -510,13 +510,16 @@ __device__ inline float group_off(const RouteParams& p, float reach, float one, 
   return apart(p) * (reach + size);
 }
 
-// Without a bias a group of one best score stands by its best logit `l`, exactly. Whether
-// any other logit's score differs from that of `l` in 64 bits too: the next one lies 2^-24 |l|
-// away or more, and so, 2^-40 at least, does its exponential as a part of itself; a sigmoid's
-// part of that is e^-l, 2^-43 at least.  Past these limits scores of 64 bits meet, as 1, as 0
-// or beside 1/2.
+// Without a bias a group of one best score stands by its best logit, exactly.  Whether
+// scores of 64 bits tell other logits from `l`: the next one lies 2^-24 |l| away or more, and
+// so, 2^-40 at least, does its exponential as a part of itself; a sigmoid's part of that is
+// e^-l, 2^-43 at least.  Past these limits scores of 64 bits meet, as 1 or as 0.
 __device__ inline bool logit_tells(const RouteParams& p, float l, float most) {
-  return fabsf(l) >= 0x1p-16f && (p.sigmoid ? l >= -600.0f && l <= 16.0f : l - most >= -600.0f);
+  return p.sigmoid ? l >= -600.0f && l <= 16.0f : l - most >= -600.0f;
+}
+// Nearer to 0 than 2^-16 logits other than `l` have to be at least twice that.
+__device__ inline bool beside_zero(float l, float other) {
+  return fabsf(l) < 0x1p-16f && other != l && fabsf(other) < 0x1p-15f;
 }
 
 // Whether a slot's score s, of exp(y), may lose places to FP32's smallest numbers, which the
@@ -610,7 +613,7 @@ __device__ inline bool choose_near(const RouteParams& p, int t, const float (&v)
       if (last && __ballot(is && rank == p.top_groups)) {
         const float l = __int_as_float(__builtin_amdgcn_readlane(
             __float_as_int(score), __ffsll((unsigned long long)last) - 1));
-        if (!logit_tells(p, l, most)) return false;
+        if (!logit_tells(p, l, most) || __ballot(is && beside_zero(l, score))) return false;
       }
     } else {  // the least that one taken can be, and the most that another can
       const float off = group_off(p, reach, one, two);
@@ -811,9 +814,9 @@ __device__ inline bool choose_rows(const RouteParams& p, int64_t t, bool there,
     });
     const bool is = score != none, in = above < p.top_groups * span;
     if (by_logit) {
-      const bool last = is && above == (p.top_groups - 1) * span;
+      const float l = row_fmax(is && above == (p.top_groups - 1) * span ? score : none);
       const bool more = row_ballot(is && !in) != 0;
-      slow = slow || (more && last && !logit_tells(p, score, most));
+      slow = slow || (more && (!logit_tells(p, l, most) || (is && beside_zero(l, score))));
     } else {  // the least that one taken can be, and the most that another can
       const float off = group_off(p, reach, one, two);
       const float least = -row_fmax(is && in ? off - score : none);

@@ -141,6 +141,20 @@ def test_distinct_logits_of_equal_scores(kind, T, E, groups, top):
         check(l, T, min(3, top * size), kind, None, groups, top, best, renorm=False)
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("E,groups,top", SHAPES)
+def test_logits_about_zero(kind, T, E, groups, top):
+    """All alike, alike but for a few, and small ones that 64 bits tell apart."""
+    gen = torch.Generator().manual_seed(E)
+    n, size = min(T, 60), E // groups
+    l = torch.zeros(n, E)
+    some = torch.tensor([0.0, -0.0, 2.0 ** -16, 2.0 ** -15, 1e-4, -1e-4, 1e-17, 1e-12])
+    for first, m in ((n // 4, 2), (n // 2, 6), (3 * n // 4, 8)):
+        l[first:] = some[:m][torch.randint(0, m, (n - first, E), generator=gen)]
+    check(l, T, min(3, top * size), kind, None, groups, top, 1, renorm=False)
+
+
 def test_two_saturated_groups():
     l = torch.tensor([[40.0, 50.0], [40.0, 41.0]])
     for T in TOKENS:
