@@ -11,9 +11,9 @@
 // past that three launches do (choose, scan, place).
 //
 // The router by groups compares sums that FP32 rounds.  It chooses in FP32 wherever the
-// error bounds tell experts and groups apart, and does the few other tokens again in 64
-// bits, so that the choice is that of 64 bits; up to 256 experts 16 lanes take a token
-// and a wave four of them.
+// bounds of every sum's own error tell experts and groups apart, and does the other tokens
+// again in 64 bits, so that the choice is that of 64 bits; up to 256 experts 16 lanes take
+// a token and a wave four of them.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -1221,7 +1221,6 @@ __global__ __launch_bounds__(256) void route_grouped_back(const RouteBackParams 
     __builtin_amdgcn_wave_barrier();
   };
   const float inverse_scale = 1.0f / p.scale;
-  // (Loads of the next tokens' slots ahead were no faster: 15 us for 14, 32768 x 256.)
   for (int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); t < p.tokens; t += step) {
     int e = -1;
     float w = 0.0f, g = 0.0f, l = 0.0f;
@@ -1318,11 +1317,13 @@ static hipError_t launch_route_of(const RouteParams& p, hipStream_t stream) {
 
 // The router by groups with a wave to each token is the shorter way as long as no wave
 // has two of them (to 2303 tokens where they are too many for one workgroup).  us of
-// four tokens to a wave and of one, 256 experts in 8 groups: 1 token 9.3 and 7.0, 8
-// tokens 9.6 and 7.7, 12 tokens 9.6 and 10.0, 48 tokens 14.5 and 24.0; in three launches
+// four tokens to a wave and of one, 256 experts in 8 groups: 1 token 9.3 and 7.1, 8
+// tokens 9.6 and 7.9, 12 tokens 9.6 and 10.0, 48 tokens 14.5 and 24.0; in three launches
 // 64 tokens 16.2 and 12.5, 1024 tokens 17.1 and 13.3, 2048 tokens 19.8 and 18.3, 4096
 // tokens 22.6 and 22.4, 8192 tokens 23.8 and 29.1; 64 experts in one group, 8 tokens 6.1
-// and 5.3, 2048 tokens 11.7 and 11.3, 4096 tokens 13.6 and 14.5.
+// and 5.3, 2048 tokens 11.7 and 11.3, 4096 tokens 13.6 and 14.5.  (How many one workgroup
+// takes is the plain router's rule, with its figures; by the ones above three launches
+// would be the shorter way for 48 tokens already.)
 static bool a_token_each(const RouteParams& p) {
   return p.tokens <= kWaves ||
          (!route_is_small(p.tokens, p.E, p.k) && route_per_block(p.tokens) <= kWaves);

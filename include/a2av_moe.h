@@ -96,7 +96,8 @@ int a2av_moe_route_backward(const void *logits, int64_t logits_stride, int64_t t
  * there are; the top_groups groups of the highest scores are taken, and of
  * their experts the k of the highest c (without a bias: of the highest logits),
  * in falling order.  Equal ones go by their lower number.  c and the groups'
- * scores are compared in 64 bits.  A logit of -inf is not chosen, nor is a c of
+ * scores are compared in 64 bits (groups by their scores without a bias, too: logits
+ * whose scores are equal there put the groups in the order of their numbers).  A logit of -inf is not chosen, nor is a c of
  * -inf; a group without any other is not taken; a token with fewer than k
  * experts to choose has empty slots.  NaN ranks above every number.
  *   weights[t][j]  scale * s of that expert, with renormalize != 0 divided by the
@@ -123,8 +124,9 @@ int a2av_moe_route_grouped(const void *logits, int64_t logits_stride, const floa
  * with mean = sum_i u_i g_i when renormalised, else 0, and 0 for every other
  * expert; softmax without renormalisation, for every expert e,
  *   dlogits[e] = softmax_e (scale * g_e - sum_i weights_i g_i)
- * with g_e = 0 where e is not chosen.  The bias gets none.  Operands, empty slots
- * and experts outside [-1, E) as in a2av_moe_route_backward; a weight of 0 gives 0. */
+ * with g_e = 0 where e is not chosen and a softmax below 2^-126 counted as 0.  The
+ * bias gets none.  Operands, empty slots and experts outside [-1, E) as in
+ * a2av_moe_route_backward; a weight of 0 gives 0. */
 int a2av_moe_route_grouped_backward(const void *logits, int64_t logits_stride, int64_t tokens,
                                     int32_t E, int32_t k, int32_t scores, int32_t renormalize,
                                     float scale, int32_t dtype, const int32_t *experts,

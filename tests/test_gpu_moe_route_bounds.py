@@ -1,7 +1,6 @@
 """The router by groups where FP32 is at its end: sums whose parts cancel, biases of the
 type's lowest value, distinct logits of equal scores, scores far below 1, and the gradient
 entry by entry, against the definition in float64."""
-import math
 
 import numpy as np
 import pytest
